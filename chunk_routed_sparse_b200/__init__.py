@@ -52,6 +52,7 @@ _lib = None
 
 # name -> (restype, argtypes); every symbol include/moc.h declares
 _I, _I64, _P, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+_POS = [_P, _I64, _I64]  # positions: pointer, batch stride, axis stride
 SIGNATURES = {
     "moc_status_string": (ctypes.c_char_p, [_I]),
     "moc_build_layout": (_I, [_P, _I, _P]),
@@ -84,6 +85,13 @@ SIGNATURES = {
     "moc_route_perturb": (_I, [_P, _I, _I, _I, _I, _P, _P, _F, _F, _I, _P, _P]),
     "moc_outer_route": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P]),
     "moc_route_masked": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P]),
+    "moc_build_rope": (_I, [_P, _P]),
+    "moc_rope_destroy": (None, [_P]),
+    "moc_rope_table": (_I, [_P, _P, _P, _I64, _P, _P]),
+    "moc_rotary": (_I, [_P, _I, _I, _I, _I64, _I, _P, _P] + _POS + [_I, _P, _P, _P]),
+    "moc_qk_norm_rope": (_I, [_P, _I, _I, _I, _I, _I64, _I] + [_P] * 8 + [_I, _F] + _POS + [_P] * 7),
+    "moc_qk_norm_rope_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I64, _I]),
+    "moc_qk_norm_rope_bwd": (_I, [_P, _I, _I, _I, _I, _I64, _I] + [_P] * 6 + [_I, _F] + _POS + [_P] * 15 + [_SZ, _P]),
 }
 
 
@@ -465,3 +473,7 @@ def check_device_error(ws: torch.Tensor) -> int:
     st = lib().moc_check_device_error(_ptr(ws), ws.numel(), ctypes.byref(det), _stream())
     _check(st, "device error word")
     return det.value
+
+
+from .rows import (QKNormRope, QKVNormRope, Rope, Rotary, qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_fwd,  # noqa: E402,F401
+                   qkv_norm_rope, qkv_norm_rope_bwd, qkv_norm_rope_fwd, rotary, rotary_bwd, rotary_fwd)

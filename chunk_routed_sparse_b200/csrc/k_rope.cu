@@ -1,0 +1,500 @@
+// Row operators in front of the attention: rotary positions, per-head RMS norms
+// of queries and keys with the rotation in the same pass, and their gradients.
+//
+//   norm:     xhat = x r,  r = 1 / sqrt(mean(x^2) + eps),  z = xhat * w
+//   rotation: (a, b) -> (a c - b s, a s + b c) on every pair, c = f cos(p w_i),
+//             s = f sin(p w_i) for the token's position p on the pair's axis
+//   gradient: g = R^T dy,  dw = sum over rows of g * xhat,
+//             dx = r (g w - xhat mean(g w xhat))
+//
+// All of it is memory-bound: the input is read once and the output written once,
+// and the re-layout from a projection's token-major rows to the attention's
+// head-major ones costs nothing more. A group of d / 8 lanes holds one row, eight
+// elements a lane, in registers; a group keeps one token and walks the heads, so
+// that the token's cosines and sines are formed once for all of them. Four rows
+// are requested before the first is used. 256 threads: 16 (d = 128) or 32 (d = 64)
+// tokens a CTA, whose outputs are one 4 KB run per head.
+//
+// Angles: the position times a 64-bit fraction of a turn, modulo 2^64, is exact
+// for every 32-bit position (an fp32 product loses 0.01 rad at position 180,000);
+// the top 32 bits go to sincospif.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "rope.cuh"
+
+namespace moc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 4;  // rows of one lane group in flight
+
+// ---- eight elements of a row -------------------------------------------------
+template <typename T>
+struct Raw {
+    static constexpr int kWords = 8 * sizeof(T) / 4;
+    uint32_t w[kWords];
+};
+
+__device__ __forceinline__ void ld16(const void* p, uint32_t* w) {
+    // plain (not read-only) path: the output may be the input itself
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p)
+                 : "memory");
+}
+
+template <typename T, bool AL>
+__device__ __forceinline__ void load_raw(const T* p, Raw<T>& r) {
+    if constexpr (AL) {
+#pragma unroll
+        for (int i = 0; i < Raw<T>::kWords; i += 4) ld16(reinterpret_cast<const uint32_t*>(p) + i, r.w + i);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = *reinterpret_cast<const volatile uint32_t*>(p + i);
+    } else {
+        const volatile uint16_t* q = reinterpret_cast<const volatile uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = uint32_t(q[2 * i]) | (uint32_t(q[2 * i + 1]) << 16);
+    }
+}
+
+template <typename T, bool AL>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T>& r) {
+    if constexpr (AL) {
+#pragma unroll
+        for (int i = 0; i < Raw<T>::kWords; i += 4)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) =
+                make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint32_t*>(p)[i] = r.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            reinterpret_cast<uint16_t*>(p)[2 * i] = uint16_t(r.w[i]);
+            reinterpret_cast<uint16_t*>(p)[2 * i + 1] = uint16_t(r.w[i] >> 16);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T>& r, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16lo(r.w[i]);
+            v[2 * i + 1] = bf16hi(r.w[i]);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void pack(const float (&v)[8], Raw<T>& r) {  // the one rounding, to nearest even
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float one(const T* p, int i) {
+    if constexpr (sizeof(T) == 4) return p[i];
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(p[i]);
+    else return __bfloat162float(p[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void load_w(const void* w, int w_fp32, int e0, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = w == nullptr ? 1.f
+               : w_fp32    ? static_cast<const float*>(w)[e0 + i]
+                           : one(static_cast<const T*>(w), e0 + i);
+}
+
+// sum over the LPR lanes of a row
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o, LPR);
+    return x;
+}
+
+// ---- rotation ----------------------------------------------------------------
+// A lane's cosines and sines. Interleaved: four pairs of its own elements. Half:
+// one pair an element, the sine signed for the element's side of the pair.
+template <bool HALF>
+struct Trig {
+    static constexpr int kN = HALF ? 8 : 4;
+    float c[kN], s[kN];
+};
+
+template <bool HALF>
+__device__ __forceinline__ void trig(const RowArgs& a, const uint64_t* turn, const uint8_t* axis, int b, int l, int e0,
+                                     Trig<HALF>& t) {
+    const int n = a.rope.pairs;
+#pragma unroll
+    for (int j = 0; j < Trig<HALF>::kN; ++j) {
+        int i;
+        bool hi = false;
+        if (HALF) {
+            i = e0 + j;
+            hi = i >= n;
+            if (hi) i -= n;
+        } else {
+            i = e0 / 2 + j;
+        }
+        t.c[j] = 1.f;
+        t.s[j] = 0.f;
+        if (i < n) {
+            const int64_t p = a.pos ? int64_t(a.pos[b * a.pos_b + axis[i] * a.pos_a + l]) : int64_t(l);
+            const uint64_t turns = uint64_t(p) * turn[i];
+            // top 32 bits as a signed fraction of a turn, in half turns [-1, 1)
+            const float x = float(int32_t(turns >> 32)) * 4.656612873077393e-10f;
+            float s, c;
+            sincospif(x, &s, &c);
+            t.c[j] = c * a.rope.factor;
+            t.s[j] = s * a.rope.factor * ((HALF && !hi) ? -a.sign : a.sign);
+        }
+    }
+}
+
+// Rotate a row in place. Elements past the rotated part keep their values (they
+// are not multiplied by one: an infinity in a partner would make that a NaN).
+template <int LPR, bool HALF>
+__device__ __forceinline__ void rotate(float (&v)[8], const Trig<HALF>& t, int n, int r, int e0) {
+    if constexpr (!HALF) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (e0 / 2 + p < n) {
+                const float x = v[2 * p], y = v[2 * p + 1];
+                v[2 * p] = x * t.c[p] - y * t.s[p];
+                v[2 * p + 1] = x * t.s[p] + y * t.c[p];
+            }
+        }
+    } else {
+        float o[8];
+        const int s = n & 7;
+        if (s == 0) {  // a lane's partners are one other lane's elements
+            const int src = e0 >= 2 * n ? r : (e0 < n ? r + (n >> 3) : r - (n >> 3));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, v[j], src, LPR);
+        } else {
+            // partners lie across two lanes: every lane offers its registers turned by
+            // s (three select steps), once in each direction
+            float up[8], dn[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) up[j] = dn[j] = v[j];
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1) {
+                float u[8], d[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = (s & k) ? up[(j + k) & 7] : up[j];
+                    d[j] = (s & k) ? dn[(j - k) & 7] : dn[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) up[j] = u[j], dn[j] = d[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float hi = __shfl_sync(0xffffffffu, up[j], ((e0 + j + n) >> 3) & (LPR - 1), LPR);
+                const float lo = __shfl_sync(0xffffffffu, dn[j], ((e0 + j - n + 8 * LPR) >> 3) & (LPR - 1), LPR);
+                o[j] = e0 + j < n ? hi : lo;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e0 + j < 2 * n) v[j] = v[j] * t.c[j] + o[j] * t.s[j];
+    }
+}
+
+__device__ __forceinline__ void tab_to_smem(const RowArgs& a, uint64_t* turn, uint8_t* axis) {
+    if (threadIdx.x < kMaxRopePairs && int(threadIdx.x) < a.rope.pairs) {
+        turn[threadIdx.x] = a.rope.turn[threadIdx.x];
+        axis[threadIdx.x] = a.rope.axis[threadIdx.x];
+    }
+    __syncthreads();
+}
+
+// ---- forward (and the rotation's transpose, with sign = -1) -------------------
+template <typename T, int D, bool HALF, bool AL>
+__global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int LPR = D / 8, TPC = kThreads / LPR;
+    __shared__ uint64_t turn[kMaxRopePairs];
+    __shared__ uint8_t axis[kMaxRopePairs];
+    tab_to_smem(a, turn, axis);
+    const int r = threadIdx.x % LPR, e0 = 8 * r;
+    const int64_t tok = int64_t(blockIdx.x) * TPC + threadIdx.x / LPR;
+    const bool live = tok < a.tokens;  // lanes past the last token work on it again and store nothing
+    const int t = live ? int(tok) : a.tokens - 1;
+    const int b = t / a.L, l = t - b * a.L;
+    Trig<HALF> tr;
+    trig<HALF>(a, turn, axis, b, l, e0, tr);
+    const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
+    int base = 0;
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {
+        const RowSec& sec = a.sec[k];
+        const int lo = max(h_lo - base, 0), hi = min(h_hi - base, sec.H);
+        base += sec.H;
+        if (lo >= hi) continue;
+        const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0;
+        T* y = static_cast<T*>(sec.y) + b * sec.ys[0] + l * sec.ys[2] + e0;
+        float w[8];
+        if (sec.mode == ROW_NORM) load_w<T>(sec.w, a.w_fp32, e0, w);
+#pragma unroll 1
+        for (int h = lo; h < hi; h += kRows) {
+            Raw<T> raw[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+                if (h + u < hi) load_raw<T, AL>(x + (h + u) * sec.xs[1], raw[u]);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                if (h + u >= hi) break;
+                if (sec.mode != ROW_COPY) {
+                    float v[8];
+                    unpack<T>(raw[u], v);
+                    if (sec.mode == ROW_NORM) {
+                        float ss = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+                        const float rs = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * w[j];
+                    }
+                    rotate<LPR, HALF>(v, tr, a.rope.pairs, r, e0);
+                    pack<T>(v, raw[u]);
+                }
+                if (live) store_raw<T, AL>(y + (h + u) * sec.ys[1], raw[u]);
+            }
+        }
+    }
+}
+
+// ---- backward of norm + rotation ---------------------------------------------
+// A persistent CTA strides over token tiles and keeps its part of dw in
+// registers; the parts of a CTA are added through shared memory in thread order
+// and those of all CTAs by rows_dw_kernel in CTA order: no atomics.
+template <typename T, int D, bool HALF, bool AL>
+__global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int LPR = D / 8, TPC = kThreads / LPR, ROWS = 2;
+    __shared__ uint64_t turn[kMaxRopePairs];
+    __shared__ uint8_t axis[kMaxRopePairs];
+    __shared__ float red[TPC][D];
+    tab_to_smem(a, turn, axis);
+    const int r = threadIdx.x % LPR, e0 = 8 * r;
+    float dw[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
+    const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
+    for (int64_t t0 = int64_t(blockIdx.x) * TPC; t0 < a.tokens; t0 += int64_t(gridDim.x) * TPC) {
+        const int64_t tok = t0 + threadIdx.x / LPR;
+        const bool live = tok < a.tokens;
+        const int t = live ? int(tok) : a.tokens - 1;
+        const int b = t / a.L, l = t - b * a.L;
+        Trig<HALF> tr;
+        trig<HALF>(a, turn, axis, b, l, e0, tr);
+        int base = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const RowSec& sec = a.sec[k];
+            const int lo = max(h_lo - base, 0), hi = min(h_hi - base, sec.H);
+            base += sec.H;
+            if (lo >= hi) continue;
+            const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0;
+            const T* g = static_cast<const T*>(sec.g) + b * sec.gs[0] + l * sec.gs[2] + e0;
+            T* y = static_cast<T*>(sec.y) + b * sec.ys[0] + l * sec.ys[2] + e0;
+            if (k == 2) {  // values: the gradient only changes its layout
+#pragma unroll 1
+                for (int h = lo; h < hi; h += kRows) {
+                    Raw<T> raw[kRows];
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u)
+                        if (h + u < hi) load_raw<T, AL>(g + (h + u) * sec.gs[1], raw[u]);
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u)
+                        if (h + u < hi && live) store_raw<T, AL>(y + (h + u) * sec.ys[1], raw[u]);
+                }
+                continue;
+            }
+            float w[8];
+            load_w<T>(sec.w, a.w_fp32, e0, w);
+#pragma unroll 1
+            for (int h = lo; h < hi; h += ROWS) {
+                Raw<T> rx[ROWS], rg[ROWS];
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    if (h + u < hi) {
+                        load_raw<T, AL>(x + (h + u) * sec.xs[1], rx[u]);
+                        load_raw<T, AL>(g + (h + u) * sec.gs[1], rg[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    if (h + u >= hi) break;
+                    float v[8], q[8];
+                    unpack<T>(rx[u], v);
+                    unpack<T>(rg[u], q);
+                    rotate<LPR, HALF>(q, tr, a.rope.pairs, r, e0);
+                    float ss = 0.f, sg = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        ss = fmaf(v[j], v[j], ss);
+                        sg = fmaf(q[j] * w[j], v[j], sg);
+                    }
+                    ss = row_sum<LPR>(ss);
+                    sg = row_sum<LPR>(sg);
+                    const float rs = rsqrtf(ss * (1.f / D) + a.eps);
+                    const float m = sg * rs * (1.f / D);  // mean(g w xhat)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float xh = v[j] * rs;
+                        if (live) dw[k][j] = fmaf(q[j], xh, dw[k][j]);
+                        v[j] = rs * (q[j] * w[j] - xh * m);
+                    }
+                    Raw<T> ry;
+                    pack<T>(v, ry);
+                    if (live) store_raw<T, AL>(y + (h + u) * sec.ys[1], ry);
+                }
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) red[threadIdx.x / LPR][e0 + j] = dw[k][j];
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float s = 0.f;
+            for (int i = 0; i < TPC; ++i) s += red[i][threadIdx.x];
+            a.part[((size_t(blockIdx.y) * gridDim.x + blockIdx.x) * 2 + k) * D + threadIdx.x] = s;
+        }
+    }
+}
+
+// dw = sum of the CTAs' parts: one CTA per weight and 32 columns, 32 runs of parts
+// added in order, then the runs in order.
+template <typename W>
+__global__ void __launch_bounds__(1024) rows_dw_kernel(int ctas, int D, const float* __restrict__ part, W* dwq, W* dwk) {
+    __shared__ float red[32][33];
+    W* out = blockIdx.y == 0 ? dwq : dwk;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.f;
+    for (int i = threadIdx.y; i < ctas; i += 32) s += part[(size_t(i) * 2 + blockIdx.y) * D + c];
+    red[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && out) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
+        if constexpr (sizeof(W) == 4) out[c] = s;
+        else if constexpr (std::is_same<W, __half>::value) out[c] = __float2half_rn(s);
+        else out[c] = __float2bfloat16_rn(s);
+    }
+}
+
+int sm_count() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+// fn<T, D, HALF, AL>(args...) for the runtime type, width, pair layout and alignment
+#define MOC_ROWS_DISPATCH(CALL)                                                     \
+    do {                                                                            \
+        const bool half = !a.rope.interleaved;                                      \
+        if (dtype == MOC_BF16) MOC_ROWS_D(__nv_bfloat16, CALL);                     \
+        else if (dtype == MOC_FP16) MOC_ROWS_D(__half, CALL);                       \
+        else MOC_ROWS_D(float, CALL);                                               \
+    } while (0)
+#define MOC_ROWS_D(T, CALL)                                                         \
+    do {                                                                            \
+        if (d == 128) MOC_ROWS_H(T, 128, CALL); else MOC_ROWS_H(T, 64, CALL);       \
+    } while (0)
+#define MOC_ROWS_H(T, D, CALL)                                                      \
+    do {                                                                            \
+        if (half) { if (aligned) CALL(T, D, true, true); else CALL(T, D, true, false); }       \
+        else { if (aligned) CALL(T, D, false, true); else CALL(T, D, false, false); }          \
+    } while (0)
+
+}  // namespace
+
+// Token tiles on x (at most `most`, CTAs stride over the rest), heads split on y
+// only while that gives fewer than four CTAs an SM: a split forms the token's
+// cosines again.
+static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t most, int* heads_per_cta) {
+    const int64_t tpc = kThreads * 8 / d, want = 4 * int64_t(sm_count());
+    int64_t tiles = (tokens + tpc - 1) / tpc;
+    int64_t split = tiles >= want ? 1 : (want + tiles - 1) / tiles;
+    if (split > heads) split = heads;
+    *heads_per_cta = int((heads + split - 1) / split);
+    if (tiles > most) tiles = most;
+    return dim3(unsigned(tiles), unsigned((heads + *heads_per_cta - 1) / *heads_per_cta));
+}
+
+static dim3 rows_bwd_grid(int d, int64_t tokens, int heads, int* heads_per_cta) {
+    return rows_grid(d, tokens, heads, 4 * int64_t(sm_count()), heads_per_cta);
+}
+
+cudaError_t launch_rows_fwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
+    RowArgs a = args;
+    const dim3 grid = rows_grid(d, a.tokens, a.heads, INT64_MAX, &a.heads_per_cta);
+#define MOC_CALL(T, D, HALF, AL) rows_fwd_kernel<T, D, HALF, AL><<<grid, kThreads, 0, s>>>(a)
+    MOC_ROWS_DISPATCH(MOC_CALL);
+#undef MOC_CALL
+    return cudaGetLastError();
+}
+
+int rows_bwd_ctas(int d, int64_t tokens, int heads) {
+    int per;
+    const dim3 g = rows_bwd_grid(d, tokens, heads, &per);
+    return int(g.x * g.y);
+}
+
+cudaError_t launch_rows_bwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
+    RowArgs a = args;
+    const dim3 grid = rows_bwd_grid(d, a.tokens, a.heads, &a.heads_per_cta);
+#define MOC_CALL(T, D, HALF, AL) rows_bwd_kernel<T, D, HALF, AL><<<grid, kThreads, 0, s>>>(a)
+    MOC_ROWS_DISPATCH(MOC_CALL);
+#undef MOC_CALL
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rows_dw(int dtype, int w_fp32, int d, int ctas, const float* part, void* dwq, void* dwk,
+                           cudaStream_t s) {
+    const dim3 grid(d / 32, 2), block(32, 32);
+    if (w_fp32 || dtype == MOC_FP32)
+        rows_dw_kernel<float><<<grid, block, 0, s>>>(ctas, d, part, static_cast<float*>(dwq), static_cast<float*>(dwk));
+    else if (dtype == MOC_FP16)
+        rows_dw_kernel<__half><<<grid, block, 0, s>>>(ctas, d, part, static_cast<__half*>(dwq), static_cast<__half*>(dwk));
+    else
+        rows_dw_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(ctas, d, part, static_cast<__nv_bfloat16*>(dwq),
+                                                             static_cast<__nv_bfloat16*>(dwk));
+    return cudaGetLastError();
+}
+
+}  // namespace moc

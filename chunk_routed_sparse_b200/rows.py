@@ -1,0 +1,394 @@
+"""Row operators in front of the attention: rotary positions, and per-head RMS
+norms of queries and keys with the rotation and the re-layout to head-major in
+the same pass (``moc_rotary``, ``moc_qk_norm_rope`` and its gradient).
+
+    rope = Rope(128, axes=(44, 42, 42))                 # time, row and column of a clip
+    Q, K, V = qkv_norm_rope(qkv, Hq, Hk, wq, wk, rope, pos)   # qkv [B, L, Hq + 2 Hk, d]
+    O = moc_attention(layout, Q, K, V, k)
+
+Tensors are [B, H, L, d] views in bf16, fp16 or fp32 whose last dim is dense, d 64
+or 128; the other dims may have any strides (token-major projections, slots of a
+cache). ``pos`` is int32 on the same device: [L] or [axes, L] for the whole batch,
+or [B, axes, L]; None counts 0 .. L-1 for a one-axis rotation. Calls run on the
+current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional, Sequence, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _check, _ptr, _stream, lib
+
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("axis_dim", ctypes.c_void_p), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("alpha", ctypes.c_double), ("beta", ctypes.c_double),
+                ("attention_factor", ctypes.c_double)]
+
+
+class Rope:
+    """A rotation of the first ``dim`` dims of every head (moc_build_rope).
+
+    axes: dims of each position axis, summing to ``dim`` (default: one axis).
+    interleaved: pairs (2i, 2i + 1), else (i, i + dim / 2). scaling: "none",
+    "linear", "ntk" or "yarn" by ``factor`` (yarn: trained at
+    ``original_length``, blended between ``alpha`` and ``beta`` turns over it,
+    the rotated part times ``attention_factor``, None for 0.1 ln(factor) + 1).
+    Holds host memory only: one plan serves every device."""
+
+    def __init__(self, dim: int, axes: Optional[Sequence[int]] = None, theta: float = 10000.0,
+                 interleaved: bool = True, scaling: str = "none", factor: float = 1.0,
+                 original_length: float = 0.0, alpha: float = 1.0, beta: float = 32.0,
+                 attention_factor: Optional[float] = None):
+        axes = (int(dim),) if axes is None else tuple(int(a) for a in axes)
+        if sum(axes) != dim:
+            raise ValueError(f"axes {axes} do not sum to {dim} rotated dims")
+        if scaling not in SCALING:
+            raise ValueError(f"unknown scaling {scaling!r}: one of {', '.join(SCALING)}")
+        if attention_factor is not None and not attention_factor > 0:
+            raise ValueError("attention_factor is positive, or None for the default")
+        arr = (ctypes.c_int32 * len(axes))(*axes)
+        desc = _RopeDesc(len(axes), ctypes.cast(arr, ctypes.c_void_p), 1 if interleaved else 0, SCALING[scaling],
+                         float(theta), float(factor), float(original_length), float(alpha), float(beta),
+                         float(attention_factor or 0.0))
+        h = ctypes.c_void_p()
+        _check(lib().moc_build_rope(ctypes.byref(desc), ctypes.byref(h)), "moc_build_rope")
+        self._h = h
+        self.dim, self.axes, self.interleaved = int(dim), axes, bool(interleaved)
+
+    @property
+    def handle(self):
+        return self._h
+
+    def table(self) -> Tuple[list, list, float]:
+        """(radians per position of every pair, its axis, factor on the rotated part)."""
+        n, f = ctypes.c_int64(), ctypes.c_double()
+        freq, axis = (ctypes.c_double * 64)(), (ctypes.c_int32 * 64)()
+        _check(lib().moc_rope_table(self._h, freq, axis, 64, ctypes.byref(n), ctypes.byref(f)), "moc_rope_table")
+        return list(freq)[:n.value], list(axis)[:n.value], f.value
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            lib().moc_rope_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _on(device: torch.device):
+    """The device's context, for the launch and its current stream."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _rows(name: str, x: torch.Tensor, like: Optional[torch.Tensor] = None, shape=None):
+    if not isinstance(x, torch.Tensor) or x.dim() != 4 or not x.is_cuda or x.dtype not in _DTYPE:
+        raise ValueError(f"{name}: expected a bf16, fp16 or fp32 CUDA tensor [B, H, L, d]")
+    if x.shape[3] not in (64, 128):
+        raise ValueError(f"{name}: d = {x.shape[3]}, expected 64 or 128")
+    if x.stride(3) != 1 and x.numel():
+        raise ValueError(f"{name}: the last dim has stride {x.stride(3)}, expected 1")
+    if like is not None and (x.dtype != like.dtype or x.device != like.device):
+        raise ValueError(f"{name}: {x.dtype} on {x.device}, expected {like.dtype} on {like.device}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+
+
+def _positions(rope: Optional[Rope], pos: Optional[torch.Tensor], B: int, L: int, d: int, device):
+    """(tensor or None, batch stride, axis stride) of the positions."""
+    if rope is None:
+        if pos is not None:
+            raise ValueError("positions without a rotation")
+        return None, 0, 0
+    if not isinstance(rope, Rope) or not rope.handle.value:
+        raise ValueError("rope: expected an open Rope")
+    if rope.dim > d:
+        raise ValueError(f"the rotation covers {rope.dim} dims, heads have {d}")
+    n = len(rope.axes)
+    if pos is None:
+        if n != 1:
+            raise ValueError(f"a rotation over {n} axes needs positions")
+        return None, 0, 0
+    if pos.dtype != torch.int32 or pos.device != device:
+        raise ValueError(f"pos: {pos.dtype} on {pos.device}, expected int32 on {device}")
+    shape = tuple(pos.shape)
+    ok = shape == (L,) and n == 1 or shape == (n, L) or shape == (B, n, L)
+    if not ok:
+        raise ValueError(f"pos: shape {shape}, expected [L], [axes, L] or [B, axes, L] for B = {B}, axes = {n}, L = {L}")
+    if L > 1 and pos.stride(-1) != 1:
+        raise ValueError("pos: the last dim is not dense")
+    return pos, pos.stride(0) if pos.dim() == 3 else 0, pos.stride(-2) if pos.dim() > 1 else 0
+
+
+def _strides(*tensors):
+    """Batch, head and token strides of every tensor in one host array, and its address."""
+    vals = []
+    for t in tensors:
+        vals += t.stride()[:3] if t is not None else (0, 0, 0)
+    buf = (ctypes.c_int64 * len(vals))(*vals)
+    return buf, ctypes.addressof(buf)
+
+
+def _rotary(rope, X, pos, transpose, out, where):
+    _rows("X", X)
+    B, H, L, d = X.shape
+    if rope is None:
+        raise ValueError("rope: expected a Rope")
+    p, pb, pa = _positions(rope, pos, B, L, d, X.device)
+    if out is None:
+        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    else:
+        _rows("out", out, X, X.shape)
+    buf, at = _strides(X, out)
+    with _on(X.device):
+        _check(lib().moc_rotary(rope.handle, _DTYPE[X.dtype], B, H, L, d, _ptr(X), at, _ptr(p), pb, pa, transpose,
+                                _ptr(out), at + 24, _stream()), where)
+    return out
+
+
+def rotary_fwd(rope: Rope, X: torch.Tensor, pos: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = R X (moc_rotary), head-major contiguous unless ``out`` says otherwise;
+    ``out`` may be X itself."""
+    return _rotary(rope, X, pos, 0, out, "moc_rotary")
+
+
+def rotary_bwd(rope: Rope, dY: torch.Tensor, pos: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dX = R^T dY, the gradient of rotary_fwd (moc_rotary, transposed)."""
+    return _rotary(rope, dY, pos, 1, out, "moc_rotary")
+
+
+def _dense(g: torch.Tensor) -> torch.Tensor:
+    return g if g.stride(-1) == 1 else g.contiguous()
+
+
+class Rotary(torch.autograd.Function):
+    """rotary_fwd with its gradient. apply(rope, X, pos) -> Y."""
+
+    @staticmethod
+    def forward(ctx, rope, X, pos):
+        ctx.rope = rope
+        ctx.save_for_backward(pos)
+        ctx.like = (X.shape, X.stride())
+        return rotary_fwd(rope, X, pos)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        shape, stride = ctx.like
+        # the gradient in the input's own order (a broadcast input: head-major, autograd adds it up)
+        dense = all(n <= 1 or s > 0 for n, s in zip(shape, stride))
+        out = torch.empty_strided(shape, stride, dtype=dY.dtype, device=dY.device) if dense and _plain(shape, stride) \
+            else None
+        return None, rotary_bwd(ctx.rope, _dense(dY), ctx.saved_tensors[0], out), None
+
+
+def _plain(shape, stride) -> bool:
+    """Whether (shape, stride) tiles its storage without holes or overlap."""
+    want = 1
+    for s, n in sorted((s, n) for n, s in zip(shape, stride) if n > 1):
+        if s != want:
+            return False
+        want *= n
+    return True
+
+
+def rotary(rope: Rope, X: torch.Tensor, pos: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable rotary positions: Y = R X, head-major contiguous."""
+    if torch.is_grad_enabled() and X.requires_grad:
+        return Rotary.apply(rope, X, pos)
+    return rotary_fwd(rope, X, pos)
+
+
+# ---- norm + rotation ---------------------------------------------------------
+def _weights(wq, wk, X, d):
+    """The weights' common type code."""
+    code = 2
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is None:
+            continue
+        if tuple(w.shape) != (d,) or not w.is_contiguous() or w.device != X.device or \
+                w.dtype not in (torch.float32, X.dtype):
+            raise ValueError(f"{name}: expected a contiguous [{d}] tensor in fp32 or {X.dtype} on {X.device}")
+        code = _DTYPE[w.dtype]
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise ValueError("wq and wk have different types")
+    return code
+
+
+def qk_norm_rope_fwd(Q, K, V=None, wq=None, wk=None, rope: Optional[Rope] = None,
+                     pos: Optional[torch.Tensor] = None, eps: float = 1e-6, out=None):
+    """Queries and keys normalised per head and rotated, values re-laid
+    (moc_qk_norm_rope). Q: [B, Hq, L, d], K and V: [B, Hk, L, d] views. Returns
+    (Qo, Ko, Vo) - Vo None without V -, head-major contiguous, or written to the
+    views of ``out`` (slots of a cache, or the inputs themselves)."""
+    _rows("Q", Q)
+    B, Hq, L, d = Q.shape
+    Hk = K.shape[1] if isinstance(K, torch.Tensor) and K.dim() == 4 else 0
+    _rows("K", K, Q, (B, Hk, L, d))
+    if V is not None:
+        _rows("V", V, Q, (B, Hk, L, d))
+    code = _weights(wq, wk, Q, d)
+    p, pb, pa = _positions(rope, pos, B, L, d, Q.device)
+    if out is None:
+        Qo = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        Ko = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
+        Vo = torch.empty(V.shape, dtype=Q.dtype, device=Q.device) if V is not None else None
+    else:
+        Qo, Ko, Vo = out
+        _rows("out Q", Qo, Q, Q.shape)
+        _rows("out K", Ko, Q, K.shape)
+        if (V is None) != (Vo is None):
+            raise ValueError("V and its output come together")
+        if V is not None:
+            _rows("out V", Vo, Q, V.shape)
+    buf, at = _strides(Q, K, V, Qo, Ko, Vo)
+    with _on(Q.device):
+        _check(lib().moc_qk_norm_rope(rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
+                                      _ptr(Q), at, _ptr(K), at + 24, _ptr(V), at + 48, _ptr(wq), _ptr(wk), code,
+                                      float(eps), _ptr(p), pb, pa, _ptr(Qo), at + 72, _ptr(Ko), at + 96, _ptr(Vo),
+                                      at + 120, _stream()), "moc_qk_norm_rope")
+    return Qo, Ko, Vo
+
+
+def qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQo, dKo, dVo=None, out=None, want_dw: bool = True):
+    """Gradient of qk_norm_rope_fwd (moc_qk_norm_rope_bwd): returns (dQ, dK, dV,
+    dwq, dwk); dQ, dK, dV head-major contiguous or in the views of ``out``; a
+    weight that is None gets None."""
+    _rows("Q", Q)
+    B, Hq, L, d = Q.shape
+    Hk = K.shape[1] if isinstance(K, torch.Tensor) and K.dim() == 4 else 0
+    _rows("K", K, Q, (B, Hk, L, d))
+    _rows("dQo", dQo, Q, Q.shape)
+    _rows("dKo", dKo, Q, K.shape)
+    if dVo is not None:
+        _rows("dVo", dVo, Q, K.shape)
+    code = _weights(wq, wk, Q, d)
+    p, pb, pa = _positions(rope, pos, B, L, d, Q.device)
+    if out is None:
+        dQ = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        dK = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
+        dV = torch.empty(K.shape, dtype=Q.dtype, device=Q.device) if dVo is not None else None
+    else:
+        dQ, dK, dV = out
+        _rows("out dQ", dQ, Q, Q.shape)
+        _rows("out dK", dK, Q, K.shape)
+        if (dVo is None) != (dV is None):
+            raise ValueError("dVo and its output come together")
+        if dV is not None:
+            _rows("out dV", dV, Q, K.shape)
+    dwq = torch.empty_like(wq) if want_dw and wq is not None else None
+    dwk = torch.empty_like(wk) if want_dw and wk is not None else None
+    buf, at = _strides(Q, K, dQo, dKo, dVo, dQ, dK, dV)
+    with _on(Q.device):
+        ws = None
+        if dwq is not None or dwk is not None:
+            n = int(lib().moc_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, d))
+            if n == 0:
+                raise ValueError("invalid problem for the workspace size query")
+            ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+        _check(lib().moc_qk_norm_rope_bwd(rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
+                                          _ptr(Q), at, _ptr(K), at + 24, _ptr(wq), _ptr(wk), code, float(eps),
+                                          _ptr(p), pb, pa, _ptr(dQo), at + 48, _ptr(dKo), at + 72, _ptr(dVo), at + 96,
+                                          _ptr(dQ), at + 120, _ptr(dK), at + 144, _ptr(dV), at + 168, _ptr(dwq),
+                                          _ptr(dwk), _ptr(ws), ws.numel() if ws is not None else 0, _stream()),
+               "moc_qk_norm_rope_bwd")
+    return dQ, dK, dV, dwq, dwk
+
+
+def _split(x: torch.Tensor, Hq: int, Hk: int):
+    """Head-major views of a packed [B, L, Hq + 2 Hk, d] projection."""
+    t = x.transpose(1, 2)
+    return t[:, :Hq], t[:, Hq:Hq + Hk], t[:, Hq + Hk:]
+
+
+def _packed(qkv, Hq, Hk):
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 4 or Hq < 1 or Hk < 1 or qkv.shape[2] != Hq + 2 * Hk:
+        raise ValueError(f"qkv: expected [B, L, Hq + 2 Hk, d] with Hq = {Hq}, Hk = {Hk}")
+    return _split(qkv, Hq, Hk)
+
+
+def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=None, eps: float = 1e-6):
+    """qk_norm_rope_fwd on the packed projection [B, L, Hq + 2 Hk, d]."""
+    Q, K, V = _packed(qkv, Hq, Hk)
+    return qk_norm_rope_fwd(Q, K, V, wq, wk, rope, pos, eps)
+
+
+def qkv_norm_rope_bwd(qkv, Hq: int, Hk: int, wq, wk, rope, pos, eps, dQ, dK, dV, want_dw: bool = True):
+    """Gradient of qkv_norm_rope_fwd: (dqkv packed and contiguous, dwq, dwk)."""
+    Q, K, _ = _packed(qkv, Hq, Hk)
+    dqkv = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
+    _, _, _, dwq, dwk = qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQ, dK, dV, _split(dqkv, Hq, Hk), want_dw)
+    return dqkv, dwq, dwk
+
+
+class QKVNormRope(torch.autograd.Function):
+    """apply(qkv, wq, wk, Hq, Hk, rope, pos, eps) -> Q, K, V with gradients for the
+    projection and the weights."""
+
+    @staticmethod
+    def forward(ctx, qkv, wq, wk, Hq, Hk, rope, pos, eps):
+        ctx.args = (Hq, Hk, rope, eps)
+        ctx.save_for_backward(qkv, wq, wk, pos)
+        return qkv_norm_rope_fwd(qkv, Hq, Hk, wq, wk, rope, pos, eps)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dQ, dK, dV):
+        qkv, wq, wk, pos = ctx.saved_tensors
+        Hq, Hk, rope, eps = ctx.args
+        want = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+        dqkv, dwq, dwk = qkv_norm_rope_bwd(qkv, Hq, Hk, wq, wk, rope, pos, eps, _dense(dQ), _dense(dK), _dense(dV), want)
+        return dqkv, dwq, dwk, None, None, None, None, None
+
+
+def qkv_norm_rope(qkv: torch.Tensor, Hq: int, Hk: int, wq: Optional[torch.Tensor] = None,
+                  wk: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                  pos: Optional[torch.Tensor] = None, eps: float = 1e-6):
+    """Differentiable: the packed projection [B, L, Hq + 2 Hk, d] to head-major Q
+    (normalised, rotated), K (the same) and V in one pass."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (qkv, wq, wk)):
+        return QKVNormRope.apply(qkv, wq, wk, Hq, Hk, rope, pos, eps)
+    return qkv_norm_rope_fwd(qkv, Hq, Hk, wq, wk, rope, pos, eps)
+
+
+class QKNormRope(torch.autograd.Function):
+    """apply(Q, K, wq, wk, rope, pos, eps) -> Qo, Ko with gradients for all four tensors."""
+
+    @staticmethod
+    def forward(ctx, Q, K, wq, wk, rope, pos, eps):
+        ctx.args = (rope, eps)
+        ctx.save_for_backward(Q, K, wq, wk, pos)
+        return qk_norm_rope_fwd(Q, K, None, wq, wk, rope, pos, eps)[:2]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dQo, dKo):
+        Q, K, wq, wk, pos = ctx.saved_tensors
+        rope, eps = ctx.args
+        want = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
+        dQ, dK, _, dwq, dwk = qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, _dense(dQo), _dense(dKo), want_dw=want)
+        return dQ, dK, dwq, dwk, None, None, None
+
+
+def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, wq: Optional[torch.Tensor] = None,
+                 wk: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                 pos: Optional[torch.Tensor] = None, eps: float = 1e-6):
+    """Differentiable norm and rotation of separate Q and K views: (Qo, Ko)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (Q, K, wq, wk)):
+        return QKNormRope.apply(Q, K, wq, wk, rope, pos, eps)
+    return qk_norm_rope_fwd(Q, K, None, wq, wk, rope, pos, eps)[:2]

@@ -415,6 +415,102 @@ moc_status moc_set_attend_kernel(int variant);
  * MOC_ERR_DEVICE_CHECK; *detail (nullable) receives a kernel-specific code. */
 moc_status moc_layout_device_error(const moc_layout* layout, int32_t* detail, moc_stream_t stream);
 
+/* ---- Operators in front of and beside the routed attention (the pages describe
+ * the attention alone; these are the steps of the same layer around it). ------- */
+
+/* Element types of the row operators below. */
+enum { MOC_BF16 = 0, MOC_FP16 = 1, MOC_FP32 = 2 };
+
+/* Stretching of a rotation past the context it was trained at, by a factor
+ * s >= 1. PLAIN: none. LINEAR: every frequency divided by s. NTK: the base raised
+ * to theta s^(n / (n - 2)) for an axis of n dims (n > 2). YARN: with
+ * t = original_length w / (2 pi) turns of a pair over the original context, the
+ * pair keeps w for t >= beta, takes w / s for t <= alpha and a linear blend
+ * between; the rotated part is multiplied by attention_factor
+ * (0: 0.1 ln s + 1). */
+enum { MOC_ROPE_PLAIN = 0, MOC_ROPE_LINEAR = 1, MOC_ROPE_NTK = 2, MOC_ROPE_YARN = 3 };
+
+/* A rotation of the first rot = axis_dim[0] + ... dims of every head (even sizes
+ * >= 2, rot <= 128; at most 4 axes: one for a running index; time, row and column
+ * for a clip). Pair i of rot / 2 belongs to the axis whose dims it falls in (axes
+ * in order), with w_j = theta^(-2j / axis_dim) for the axis's pair j; it joins
+ * dims (2i, 2i + 1) when interleaved != 0 and (i, i + rot / 2) when 0:
+ * (a, b) -> (a cos pw - b sin pw, a sin pw + b cos pw). Dims past rot pass
+ * through unchanged. theta > 1. */
+typedef struct {
+    int32_t n_axes;
+    const int32_t* axis_dim;
+    int32_t interleaved;
+    int32_t scaling;          /* MOC_ROPE_* */
+    double theta;
+    double factor;            /* s (not read for PLAIN) */
+    double original_length;   /* YARN, and the four below */
+    double alpha, beta;
+    double attention_factor;
+} moc_rope_desc;
+
+typedef struct moc_rope moc_rope; /* opaque; host memory only, usable on every device */
+
+moc_status moc_build_rope(const moc_rope_desc* desc, moc_rope** out);
+void moc_rope_destroy(moc_rope* rope);
+
+/* The pairs' angle per position in radians and their axes (min(count, cap)
+ * entries; freq and axis may be NULL), their number, and the factor on the
+ * rotated part (nullable). */
+moc_status moc_rope_table(const moc_rope* rope, double* freq, int32_t* axis, int64_t cap, int64_t* count,
+                          double* factor);
+
+/* Tensors of the row operators: [B][H][L][d] of dtype (MOC_BF16, MOC_FP16 or
+ * MOC_FP32) with strides of batch, head and token in elements (int64[3], host
+ * memory, read during the call; the last dim is dense), d 64 or 128, in any
+ * order of the first three - a projection's token-major rows, a packed
+ * projection's parts, a cache's slots, head-major tensors. Rows on 16-byte
+ * boundaries take 16-byte accesses, others narrower ones. An output may be its
+ * own input (same pointer and strides); any other overlap is undefined. An input
+ * may have strides of 0 (a broadcast), an output may not. Sums and the rotation
+ * are in fp32, with one rounding at the end.
+ * pos: device int32 positions, pos[b * pos_batch + axis * pos_axis + l] (pos_batch
+ * 0: shared by the batch); NULL with a one-axis rotation: 0 .. L-1. Any int32
+ * position, negative ones included; angles are reduced exactly, so far positions
+ * lose nothing. B * L < 2^31 - 256, at most 65535 heads in all. */
+
+/* Y = R X, or R^T X with transpose != 0 (the rotation's gradient: for
+ * Y = R X, dX = R^T dY). */
+moc_status moc_rotary(const moc_rope* rope, int dtype, int B, int H, int64_t L, int d, const void* X,
+                      const int64_t* x_strides, const int32_t* pos, int64_t pos_batch, int64_t pos_axis,
+                      int transpose, void* Y, const int64_t* y_strides, moc_stream_t stream);
+
+/* Queries and keys normalised per head and rotated, values re-laid, in one pass:
+ *   Qo = R(wq * Q / sqrt(mean(Q^2) + eps)),  Ko the same with K, wk,  Vo = V,
+ * the mean over the d dims of each row. Q, Qo: Hq heads; K, V, Ko, Vo: Hk heads.
+ * V and Vo may both be NULL. rope NULL: no rotation. wq, wk: device [d] in fp32
+ * or dtype (w_dtype), NULL for ones. eps >= 0. */
+moc_status moc_qk_norm_rope(const moc_rope* rope, int dtype, int B, int Hq, int Hk, int64_t L, int d, const void* Q,
+                            const int64_t* q_strides, const void* K, const int64_t* k_strides, const void* V,
+                            const int64_t* v_strides, const void* wq, const void* wk, int w_dtype, float eps,
+                            const int32_t* pos, int64_t pos_batch, int64_t pos_axis, void* Qo,
+                            const int64_t* qo_strides, void* Ko, const int64_t* ko_strides, void* Vo,
+                            const int64_t* vo_strides, moc_stream_t stream);
+
+/* Bytes of device workspace moc_qk_norm_rope_bwd needs on the current device
+ * (0 on invalid arguments). */
+size_t moc_qk_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t L, int d);
+
+/* Gradient of moc_qk_norm_rope from its inputs and the gradients of its outputs:
+ * with g = R^T dQo, xhat = Q r, r = 1 / sqrt(mean(Q^2) + eps),
+ *   dQ = r (g wq - xhat mean(g wq xhat)),  dwq = sum over rows of g xhat
+ * (fp32 sums, written in w_dtype), dK and dwk the same, dV = dVo re-laid (dVo and
+ * dV may both be NULL). dwq, dwk nullable; ws (256-byte aligned) is read only
+ * when one is wanted. Deterministic on one device model. */
+moc_status moc_qk_norm_rope_bwd(const moc_rope* rope, int dtype, int B, int Hq, int Hk, int64_t L, int d,
+                                const void* Q, const int64_t* q_strides, const void* K, const int64_t* k_strides,
+                                const void* wq, const void* wk, int w_dtype, float eps, const int32_t* pos,
+                                int64_t pos_batch, int64_t pos_axis, const void* dQo, const int64_t* dqo_strides,
+                                const void* dKo, const int64_t* dko_strides, const void* dVo,
+                                const int64_t* dvo_strides, void* dQ, const int64_t* dq_strides, void* dK,
+                                const int64_t* dk_strides, void* dV, const int64_t* dv_strides, void* dwq, void* dwk,
+                                void* ws, size_t ws_bytes, moc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
