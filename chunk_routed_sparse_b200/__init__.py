@@ -52,6 +52,7 @@ _lib = None
 
 # name -> (restype, argtypes); every symbol include/moc.h declares
 _I, _I64, _P, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+_WIN = [_I64, _I64, _I64, _I, _P, _P, _F]  # left, right, sinks, causal, q_len, kv_len, scale
 _POS = [_P, _I64, _I64]  # positions: pointer, batch stride, axis stride
 SIGNATURES = {
     "moc_status_string": (ctypes.c_char_p, [_I]),
@@ -85,6 +86,8 @@ SIGNATURES = {
     "moc_route_perturb": (_I, [_P, _I, _I, _I, _I, _P, _P, _F, _F, _I, _P, _P]),
     "moc_outer_route": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P]),
     "moc_route_masked": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P]),
+    "moc_window_attention": (_I, [_I, _I, _I, _I64, _I64, _I, _P, _P, _P] + _WIN + [_P, _P, _P]),
+    "moc_window_device_error": (_I, [_P, _P]),
     "moc_build_rope": (_I, [_P, _P]),
     "moc_rope_destroy": (None, [_P]),
     "moc_rope_table": (_I, [_P, _P, _P, _I64, _P, _P]),
@@ -477,3 +480,4 @@ def check_device_error(ws: torch.Tensor) -> int:
 
 from .rows import (QKNormRope, QKVNormRope, Rope, Rotary, qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_fwd,  # noqa: E402,F401
                    qkv_norm_rope, qkv_norm_rope_bwd, qkv_norm_rope_fwd, rotary, rotary_bwd, rotary_fwd)
+from .window import check_window_error, window_attention_fwd  # noqa: E402,F401

@@ -1,0 +1,504 @@
+// Sliding-window attention with always-visible first keys, forward, on the
+// 5th-generation tensor cores.
+//
+//   O_t = sum_u softmax_u(scale q_t . k_u) v_u over the row's visible keys
+//   (window.cuh), lse_t = log sum_u exp(scale q_t . k_u);
+//   a row that sees no key: O = 0, lse = -inf.
+//
+// One persistent CTA per SM walks work items (256 consecutive rows of a head, two
+// 128-row tiles A and B that share one key stream) in a fixed order: no counter in
+// memory, so calls on different streams and captured graphs share nothing.
+//   warp 8 (one lane): TMA of Q tiles and of 128-key K and V tiles (2-stage rings).
+//   warp 9 (one lane): S_q = Q K^T and O_q += P V (P from TMEM), alternating A and
+//          B; an item's last PV and the next item's first S are issued back to back.
+//   warps 0-3 / 4-7: softmax of tile A / B, one thread a row, running max and sum
+//          in fp32, P written over S as bf16 (a rounding of 2^-9 of each weight; the
+//          sum is of the unrounded weights); the epilogue stages O through shared
+//          memory into whole 128-byte row pieces.
+// A tile that one of A, B cannot see is skipped for it; a tile that every row of a
+// warp sees whole takes no masking. Keys past a tile's end are other rows' or none:
+// their scores become -inf and their V rows are zeroed in shared memory (0 x NaN).
+// Every wait is bounded (2 s): a wait that gives up records itself in the error
+// word of moc_window_device_error and every role leaves.
+#include "common.cuh"
+#include "pipeline.cuh"
+#include "tmap.cuh"
+#include "window.cuh"
+
+namespace moc {
+
+// error code and detail of the window kernels on this device
+__device__ int32_t g_window_err[4];
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kRowsItem = 256;
+// launched at 168 registers a thread (384 x 168 = 64512): softmax warpgroups 216,
+// the loading / issuing one 72: 2 x 128 x 216 + 128 x 72 = 64512
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLazy = 8.f;  // O is rescaled once the row max grows by more than 2^8
+
+template <int D>
+struct Cfg {
+    static constexpr int kSlabs = D / 64;
+    static constexpr int kSlabBytes = 128 * 128;
+    static constexpr int kTileBytes = kSlabs * kSlabBytes;
+    static constexpr int oQ = 0;
+    static constexpr int oK = oQ + 2 * kTileBytes;
+    static constexpr int oV = oK + 2 * kTileBytes;
+    static constexpr int oStage = oV + 2 * kTileBytes;  // 8 warps x 32 rows x 128 B
+    static constexpr int oBar = oStage + 8 * 4096;
+    // + alignment slack; at least 120 KB so that one CTA owns an SM and its TMEM
+    static constexpr int kSmem = (oBar + 256 + 1024) > 120 * 1024 ? (oBar + 256 + 1024) : 120 * 1024;
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+    static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0);
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 1);
+};
+
+__device__ __forceinline__ uint32_t col_s(int q) { return q ? 128u : 0u; }
+__device__ __forceinline__ uint32_t col_o(int q) { return q ? 384u : 256u; }
+
+enum {
+    B_Q_FULL = 0, B_Q_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 6, B_V_FULL = 8, B_V_EMPTY = 10, B_S_FULL = 12,
+    B_P_FULL = 14, B_PV_DONE = 16, B_MMA_DONE = 18, B_COUNT = 19
+};
+struct Shared {  // at oBar + 160
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(B_COUNT * 8 <= 160, "barriers");
+
+// An item, and one of its two row tiles. Each role keeps the tiles in scalars (an
+// index that the compiler cannot see through would put them in local memory).
+struct Item {
+    int b, hq, t0;    // first row
+    int end;          // one past the last live row (<= t0: none)
+    win::Seq seq;
+    win::Span all;    // key tiles
+    int tiles;
+};
+struct QTile {
+    int rows;         // live rows
+    win::Span y;
+    int last;         // the item's last key tile that it sees (-1: none)
+    __device__ __forceinline__ bool sees(int key0, int end) const { return last >= 0 && win::meets(y, key0, end); }
+};
+
+// Items of one position range lie next to each other over the heads; the last rows
+// (the longest spans under an open causal window) come first.
+__device__ __forceinline__ void decode(const WinArgs& a, int nqt, int item, Item& x) {
+    const int heads = a.B * a.Hq;
+    const int qt = nqt - 1 - item / heads, bh = item % heads;
+    x.b = bh / a.Hq;
+    x.hq = bh - x.b * a.Hq;
+    x.t0 = qt * kRowsItem;
+    x.seq = win::seq(a, x.b);
+    x.end = min(x.t0 + kRowsItem, x.seq.m);
+    x.all = win::Span{0, 0, 0, 0, 0};
+    if (x.end > x.t0) x.all = win::span(a, x.seq, x.t0, x.end);
+    x.tiles = x.all.na + x.all.nb;
+}
+__device__ __forceinline__ QTile tile_of(const WinArgs& a, const Item& x, int q) {
+    QTile t;
+    const int r0 = x.t0 + 128 * q, r1 = min(r0 + 128, x.end);
+    t.rows = max(r1 - r0, 0);
+    t.y = win::Span{0, 0, 0, 0, 0};
+    t.last = -1;
+    if (t.rows > 0) {
+        t.y = win::span(a, x.seq, r0, r1);
+        const int key = max(t.y.a1, t.y.b1) - 1;  // its last key lies in one of the item's runs
+        if (key >= 0) t.last = x.all.nb > 0 && key >= x.all.b0 ? x.all.na + (key - x.all.b0) / win::kTile : key / win::kTile;
+    }
+    return t;
+}
+// The k-th item of a CTA: rounds over the grid, every other one backwards, so that
+// no CTA gets the longer item of every round.
+__device__ __forceinline__ int nth_item(int k) {
+    const int g = int(gridDim.x), i = int(blockIdx.x);
+    return k * g + ((k & 1) ? g - 1 - i : i);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WinArgs a, int n_items, int nqt,
+                      __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base + C::oQ, sK = base + C::oK, sV = base + C::oV, sBar = base + C::oBar;
+    Shared& sh = *reinterpret_cast<Shared*>(gbase + C::oBar + 160);
+    volatile int* abort = &sh.abort;
+    int32_t* hdr = g_window_err;
+    auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1) ? 128 : 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    const int n_rounds = (n_items + int(gridDim.x) - 1) / int(gridDim.x);
+
+    if (warp >= 8) {
+        regs_dec<kRegsOther>();
+        if (warp == 8 && lane == 0) {
+            // ---------------------------------------------------------- loads
+            prefetch_tmap(&tmQ);
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+            uint32_t gk = 0, gv = 0, nq[2] = {0, 0};
+            bool stop = false;
+            for (int k = 0; k < n_rounds && !stop; ++k) {
+                const int item = nth_item(k);
+                if (item >= n_items) continue;
+                Item x;
+                decode(a, nqt, item, x);
+                const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
+                const int qrow = (x.b * a.Hq + x.hq) * a.Lq + x.t0;
+                const int krow = (x.b * a.Hk + x.hq / a.group) * a.Lk;
+                bool have[2] = {false, false};
+                for (int j = 0; j < x.tiles && !stop; ++j) {
+                    int key0, end;
+                    win::tile(x.all, j, key0, end);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {  // a Q tile arrives with the first key tile that it sees
+                        if (have[q] || !qt[q].sees(key0, end)) continue;
+                        have[q] = true;
+                        if (!wait_bar(bar(B_Q_EMPTY + q), (nq[q] & 1) ^ 1, abort, hdr, 201)) { stop = true; break; }
+                        ++nq[q];
+                        mbar_expect_tx(bar(B_Q_FULL + q), C::kTileBytes);
+#pragma unroll
+                        for (int s = 0; s < C::kSlabs; ++s)
+                            tma_load_2d(sQ + q * C::kTileBytes + s * C::kSlabBytes, &tmQ, bar(B_Q_FULL + q), 64 * s,
+                                        qrow + 128 * q);
+                    }
+                    if (stop) break;
+                    const uint32_t st = gk & 1, sv = gv & 1;
+                    if (!wait_bar(bar(B_K_EMPTY + st), ((gk >> 1) & 1) ^ 1, abort, hdr, 202)) { stop = true; break; }
+                    mbar_expect_tx(bar(B_K_FULL + st), C::kTileBytes);
+#pragma unroll
+                    for (int s = 0; s < C::kSlabs; ++s)
+                        tma_load_2d(sK + st * C::kTileBytes + s * C::kSlabBytes, &tmK, bar(B_K_FULL + st), 64 * s,
+                                    krow + key0);
+                    ++gk;
+                    if (!wait_bar(bar(B_V_EMPTY + sv), ((gv >> 1) & 1) ^ 1, abort, hdr, 203)) { stop = true; break; }
+                    mbar_expect_tx(bar(B_V_FULL + sv), C::kTileBytes);
+#pragma unroll
+                    for (int s = 0; s < C::kSlabs; ++s)
+                        tma_load_2d(sV + sv * C::kTileBytes + s * C::kSlabBytes, &tmV, bar(B_V_FULL + sv), 64 * s,
+                                    krow + key0);
+                    ++gv;
+                }
+            }
+            // every issued copy lands before the CTA exits
+            for (uint32_t g = gk >= 2 ? gk - 2 : 0; g < gk; ++g) drain_bar(bar(B_K_FULL + (g & 1)), (g >> 1) & 1, hdr, 204);
+            for (uint32_t g = gv >= 2 ? gv - 2 : 0; g < gv; ++g) drain_bar(bar(B_V_FULL + (g & 1)), (g >> 1) & 1, hdr, 205);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (nq[q] > 0) drain_bar(bar(B_Q_FULL + q), (nq[q] - 1) & 1, hdr, 206);
+        } else if (warp == 9 && lane == 0) {
+            // ---------------------------------------------------------- MMA issue
+            uint32_t gt = 0;                 // key tiles
+            uint32_t np[2] = {0, 0};         // tiles of A / B (S_FULL, P_FULL, PV_DONE phases)
+            uint32_t nq[2] = {0, 0};         // Q tiles
+            bool pend[2] = {false, false};   // S issued for the previous key tile, PV outstanding
+            bool fresh[2] = {false, false};  // that PV is the item's first
+            bool stop = false;
+            // O_q += P_q V of the previous key tile
+            auto issue_pv = [&](int q) -> bool {
+                const uint32_t pst = (gt - 1) & 1;
+                if (!wait_bar(bar(B_P_FULL + q), (np[q] - 1) & 1, abort, hdr, 211)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_ts(tmem + col_o(q), tmem + col_s(q) + kk * 8,
+                            sdesc_sw128(sV + pst * C::kTileBytes + kk * 2048, C::kSlabBytes, 1024), C::kIdescPV,
+                            (!fresh[q] || kk > 0));
+                umma_commit(bar(B_PV_DONE + q));
+                pend[q] = fresh[q] = false;
+                return true;
+            };
+            for (int k = 0; k < n_rounds && !stop; ++k) {
+                const int item = nth_item(k);
+                if (item >= n_items) continue;
+                Item x;
+                decode(a, nqt, item, x);
+                const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
+                bool have[2] = {false, false};
+                for (int j = 0; j < x.tiles; ++j) {
+                    int key0, end;
+                    win::tile(x.all, j, key0, end);
+                    const uint32_t st = gt & 1;
+                    if (gt > 0 && !wait_bar(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 212)) { stop = true; break; }
+                    bool k_ready = false;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (pend[q] && !issue_pv(q)) { stop = true; break; }
+                        if (!k_ready) {
+                            if (!wait_bar(bar(B_K_FULL + st), (gt >> 1) & 1, abort, hdr, 213)) { stop = true; break; }
+                            k_ready = true;
+                        }
+                        if (!qt[q].sees(key0, end)) continue;
+                        if (!have[q]) {
+                            if (!wait_bar(bar(B_Q_FULL + q), nq[q] & 1, abort, hdr, 214)) { stop = true; break; }
+                            have[q] = fresh[q] = true;
+                            ++nq[q];
+                        }
+                        tc_fence_after();
+                        const uint32_t qb = sQ + q * C::kTileBytes, kb = sK + st * C::kTileBytes;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
+                            umma_ss(tmem + col_s(q), sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
+                                    C::kIdescQK, kk > 0);
+                        }
+                        umma_commit(bar(B_S_FULL + q));
+                        pend[q] = true;
+                        ++np[q];
+                        if (j == qt[q].last) umma_commit(bar(B_Q_EMPTY + q));  // its Q rows may be replaced
+                    }
+                    if (stop) break;
+                    if (gt > 0) umma_commit(bar(B_V_EMPTY + ((gt - 1) & 1)));
+                    umma_commit(bar(B_K_EMPTY + st));
+                    ++gt;
+                }
+            }
+            if (!stop && gt > 0) {
+                if (wait_bar(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 215)) {
+                    bool ok = !pend[0] || issue_pv(0);
+                    if (ok && pend[1]) issue_pv(1);
+                }
+            }
+            umma_commit(bar(B_MMA_DONE));  // TMEM is released after every MMA
+            drain_bar(bar(B_MMA_DONE), 0, hdr, 216);
+        }
+        __syncwarp();
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // -------------------------------------------------------------- softmax
+        const int q = warp >> 2, row = tid & 127;
+        const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t s_addr = lane_addr + col_s(q), o_addr = lane_addr + col_o(q);
+        const uint32_t stg = base + C::oStage + warp * 4096;
+        const float sl2 = a.scale * 1.4426950408889634f;
+        uint32_t gt = 0, np = 0;
+        bool stop = false;
+        for (int k = 0; k < n_rounds && !stop; ++k) {
+            const int item = nth_item(k);
+            if (item >= n_items) continue;
+            Item x;
+            decode(a, nqt, item, x);
+            const QTile qt = tile_of(a, x, q);
+            if (qt.rows == 0) {
+                gt += x.tiles;
+                continue;
+            }
+            const int t = x.t0 + 128 * q + row;
+            const bool live = row < qt.rows;
+            const win::Row vis = win::row(a, x.seq.n, t + x.seq.shift);
+            float m_used = -INFINITY, l = 0.f;
+            bool any = false;
+            for (int j = 0; j < x.tiles; ++j, ++gt) {
+                int key0, end;
+                win::tile(x.all, j, key0, end);
+                if (!qt.sees(key0, end)) continue;
+                if (!wait_bar_warp(bar(B_S_FULL + q), np & 1, abort, hdr, 221)) { stop = true; break; }
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
+                tmem_wait_ld_regs(s);
+                const int ns = min(vis.s, end) - key0, lo = vis.lo - key0, hi = min(vis.hi, end) - key0;
+                if (!__all_sync(0xffffffffu, !live || ns >= 128 || (lo <= 0 && hi >= 128))) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t keep = win::bits(0, ns - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(keep & (1u << c))) s[32 * w + c] = 0xff800000u;  // -inf
+                    }
+                }
+                float mv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mv[i] = fmaxf(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+#pragma unroll
+                for (int c = 16; c < 128; c += 16) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mv[i] = max3(mv[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+                }
+                const float mx = max3(max3(mv[0], mv[1], mv[2]), max3(mv[3], mv[4], mv[5]), fmaxf(mv[6], mv[7])) * sl2;
+                float alpha = 1.f;
+                bool rescale = false;
+                if (mx > m_used + kLazy) {  // also the first visible key: nothing to rescale then
+                    if (m_used > -INFINITY) {
+                        alpha = ex2(m_used - mx);
+                        rescale = true;
+                    }
+                    m_used = mx;
+                }
+                if (__any_sync(0xffffffffu, rescale)) {  // warp-collective TMEM access; alpha = 1 elsewhere
+                    if (!wait_bar_warp(bar(B_PV_DONE + q), (np - 1) & 1, abort, hdr, 222)) { stop = true; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_addr + c * 32, o);
+                        tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(o_addr + c * 32, o);
+                    }
+                }
+                // a row without a visible key so far: its weights are exp2(-inf - 0) = 0
+                const float m0 = m_used > -INFINITY ? m_used : 0.f;
+                const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m0, -m0);
+                uint64_t sum2a = 0, sum2b = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const int e = h * 64 + 2 * c;
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, nm2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        if (c & 1) sum2b = f2_add(sum2b, f2_pack(p0, p1));
+                        else sum2a = f2_add(sum2a, f2_pack(p0, p1));
+                        pk[c] = pack_bf16(p0, p1);
+                    }
+                    tmem_st32(s_addr + h * 32, pk);
+                }
+                float r0, r1, r2, r3;
+                f2_unpack(sum2a, r0, r1);
+                f2_unpack(sum2b, r2, r3);
+                l = l * alpha + ((r0 + r1) + (r2 + r3));
+                if (end - key0 < 128) {  // V rows past the tile's keys: zeros, whatever was loaded
+                    if (!wait_bar_warp(bar(B_V_FULL + (gt & 1)), (gt >> 1) & 1, abort, hdr, 223)) { stop = true; break; }
+                    if (row >= end - key0) {
+                        const uint32_t vr = sV + (gt & 1) * C::kTileBytes + row * 128;
+#pragma unroll
+                        for (int i = 0; i < C::kSlabs * 8; ++i)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vr + (i >> 3) * C::kSlabBytes + (i & 7) * 16),
+                                         "r"(0u) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(B_P_FULL + q));
+                ++np;
+                any = true;
+            }
+            if (stop) break;
+            // ---------------------------------------------------------- epilogue
+            const size_t orow = (size_t(x.b) * a.Hq + x.hq) * size_t(a.Lq) + size_t(x.t0 + 128 * q);
+            if (any) {
+                if (!wait_bar_warp(bar(B_PV_DONE + q), (np - 1) & 1, abort, hdr, 224)) break;
+                tc_fence_after();
+            }
+            const bool seen = l > 0.f || l != l;  // NaN stays NaN
+            const float inv = 1.f / l;
+            const int w0 = (warp & 3) * 32;
+            __nv_bfloat16* out = O + (orow + w0) * D;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t o[32];
+                    if (any) {
+                        tmem_ld32(o_addr + c * 64 + hh * 32, o);
+                        tmem_wait_ld_regs(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        pk[hh * 16 + i] = seen ? pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                                 "r"(pk[4 * i]), "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3]) : "memory");
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3), ch = lane & 7;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(stg + r * 128 + ((ch ^ (r & 7)) << 4)) : "memory");
+                    if (w0 + r < qt.rows) *reinterpret_cast<uint4*>(out + size_t(r) * D + c * 64 + ch * 8) = v;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            if (live && lse) lse[orow + row] = seen ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void* V, void* O, float* lse,
+                     cudaStream_t s) {
+    CUtensorMap tmQ, tmK, tmV;
+    const int64_t qrows = int64_t(a.B) * a.Hq * a.Lq, krows = int64_t(a.B) * a.Hk * a.Lk;
+    if (!make_tmap(&tmQ, Q, D, qrows)) return cudaErrorInvalidValue;
+    if (krows == 0) tmK = tmV = tmQ;  // no key tile is loaded
+    else if (!make_tmap(&tmK, K, D, krows) || !make_tmap(&tmV, V, D, krows)) return cudaErrorInvalidValue;
+    const int smem = Cfg<D>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int nqt = (a.Lq + kRowsItem - 1) / kRowsItem;
+    const int n_items = a.B * a.Hq * nqt;
+    window_fwd_kernel<D><<<n_items < sms ? n_items : sms, kThreads, smem, s>>>(
+        tmQ, tmK, tmV, a, n_items, nqt, static_cast<__nv_bfloat16*>(O), lse);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
+                              float* lse, cudaStream_t s) {
+    return d == 128 ? launch_d<128>(a, Q, K, V, O, lse, s) : launch_d<64>(a, Q, K, V, O, lse, s);
+}
+
+}  // namespace moc
+
+extern "C" moc_status moc_window_device_error(int32_t* detail, moc_stream_t stream) {
+    int32_t h[2] = {0, 0};
+    cudaStream_t s = (cudaStream_t)stream;
+    if (cudaMemcpyFromSymbolAsync(h, moc::g_window_err, sizeof h, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess)
+        return MOC_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return MOC_ERR_CUDA;
+    if (detail) *detail = h[0] != moc::ERR_NONE ? h[1] : 0;
+    if (h[0] == moc::ERR_NONE) return MOC_OK;
+    const int32_t zero[2] = {0, 0};
+    if (cudaMemcpyToSymbolAsync(moc::g_window_err, zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess)
+        return MOC_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return MOC_ERR_CUDA;
+    return h[0] == moc::ERR_TIMEOUT ? MOC_ERR_DEVICE_TIMEOUT : MOC_ERR_DEVICE_CHECK;
+}

@@ -1,0 +1,82 @@
+"""Attention with a sliding window and always-visible first keys
+(``moc_window_attention`` and its gradient).
+
+    O = window_attention(Q, K, V, left=1560, right=1560, sinks=512)        # captions and a frame either side
+    O = window_attention(Q, K, V, left=4095, sinks=64, causal=True)        # a causal window
+    O, lse = window_attention_fwd(q, cache_k, cache_v, 4095, 0, 64, True, kv_len=lens)   # one new token a stream
+
+Q, O: contiguous bf16 [B, Hq, Lq, d]; K, V: [B, Hk, Lk, d], Hk dividing Hq, d 64 or
+128. Row t of batch entry b is at position p = t + kv_len[b] - q_len[b] and sees key
+u < kv_len[b] iff (not causal or u <= p) and (u < sinks or p - left <= u <= p + right);
+a negative left or right is no limit. q_len, kv_len: int32 [B] on the device, None for
+Lq, Lk. Calls run on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import _check, _ptr, _stream, lib
+from .rows import _on
+
+
+def _tensor(name, x, shape, device, dtype=torch.bfloat16):
+    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.device != device or tuple(x.shape) != tuple(shape) or \
+            not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def _problem(Q, K, V, q_len, kv_len):
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or not Q.is_cuda:
+        raise ValueError("Q: expected a bf16 CUDA tensor [B, Hq, Lq, d]")
+    B, Hq, Lq, d = Q.shape
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("K: expected a bf16 CUDA tensor [B, Hk, Lk, d]")
+    Hk, Lk = K.shape[1], K.shape[2]
+    if d not in (64, 128):
+        raise ValueError(f"d = {d}, expected 64 or 128")
+    if (Hk == 0) != (Hq == 0) or (Hk and Hq % Hk):
+        raise ValueError(f"{Hk} key heads do not divide {Hq} query heads")
+    _tensor("Q", Q, Q.shape, Q.device)
+    _tensor("K", K, (B, Hk, Lk, d), Q.device)
+    _tensor("V", V, (B, Hk, Lk, d), Q.device)
+    for name, x in (("q_len", q_len), ("kv_len", kv_len)):
+        if x is not None:
+            _tensor(name, x, (B,), Q.device, torch.int32)
+    return B, Hq, Hk, Lq, Lk, d
+
+
+def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, causal: bool = False,
+                         q_len: Optional[torch.Tensor] = None, kv_len: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, O: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None):
+    """(O, lse) (moc_window_attention). Rows past q_len are left as they were in a
+    given O or lse, and are 0 and -inf in new ones."""
+    B, Hq, Hk, Lq, Lk, d = _problem(Q, K, V, q_len, kv_len)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if O is None:
+        O = torch.empty_like(Q) if q_len is None else torch.zeros_like(Q)
+    else:
+        _tensor("O", O, Q.shape, Q.device)
+    if lse is None:
+        lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=Q.device)
+        if q_len is not None:
+            lse.fill_(-math.inf)
+    else:
+        _tensor("lse", lse, (B, Hq, Lq), Q.device, torch.float32)
+    with _on(Q.device):
+        _check(lib().moc_window_attention(B, Hq, Hk, Lq, Lk, d, _ptr(Q), _ptr(K), _ptr(V), left, right, sinks,
+                                          1 if causal else 0, _ptr(q_len), _ptr(kv_len), float(scale), _ptr(O),
+                                          _ptr(lse), _stream()), "moc_window_attention")
+    return O, lse
+
+
+def check_window_error() -> int:
+    """Read and clear the current device's error word of the window calls
+    (synchronises); raises MocError on a recorded device error."""
+    det = ctypes.c_int32()
+    _check(lib().moc_window_device_error(ctypes.byref(det), _stream()), "window device error word")
+    return det.value

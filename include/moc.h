@@ -511,6 +511,36 @@ moc_status moc_qk_norm_rope_bwd(const moc_rope* rope, int dtype, int B, int Hq, 
                                 const int64_t* dk_strides, void* dV, const int64_t* dv_strides, void* dwq, void* dwk,
                                 void* ws, size_t ws_bytes, moc_stream_t stream);
 
+/* Attention with a sliding window and always-visible first keys, at token
+ * granularity (the routed attention's anchors are whole chunks; this is the local
+ * attention that a layer without routing, or a stream of new tokens, uses).
+ * Q, O: device bf16 [B][Hq][Lq][d]; K, V: device bf16 [B][Hk][Lk][d], contiguous,
+ * 16-byte aligned, d 64 or 128; Hk divides Hq (query head h reads key head
+ * h / (Hq / Hk)). q_len, kv_len: device int32 [B], NULL for Lq and Lk; values are
+ * clamped to [0, Lq] and [0, Lk]. Of batch entry b, row t < m = q_len[b] is at
+ * position p = t + n - m with n = kv_len[b] keys (the rows are the last m tokens of
+ * the stream: n = m for a padded batch, m = 1 for one new token), and sees key
+ * u < n iff
+ *   (causal == 0 or u <= p) and (u < sinks or p - left <= u <= p + right),
+ * left < 0 or right < 0: no limit on that side. O is the softmax of the scaled
+ * scores over the visible keys applied to V, rounded once to bf16; lse (nullable)
+ * fp32 [B][Hq][Lq] their log-sum-exp. A row that sees no key gets O = 0 and
+ * lse = -inf. Rows t >= q_len[b] of O and lse are left as they were, and keys
+ * that no row sees are not read into any result, whatever they hold. (A key
+ * that only some rows of 256 see, and that holds an infinity or a NaN, can reach
+ * the others as 0 x infinity.) softmax_scale > 0, finite. Lq, Lk < 2^29,
+ * B Hq Lq and B Hk Lk < 2^31, B and Hq at most 65535. Asynchronous, no
+ * workspace; a device-side wait that gives up is reported by
+ * moc_window_device_error. */
+moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q, const void* K,
+                                const void* V, int64_t left, int64_t right, int64_t sinks, int causal,
+                                const int32_t* q_len, const int32_t* kv_len, float softmax_scale, void* O,
+                                float* lse, moc_stream_t stream);
+
+/* Read and clear the current device's error word of the window calls, as
+ * moc_check_device_error does for a workspace. Synchronises the stream. */
+moc_status moc_window_device_error(int32_t* detail, moc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,125 @@
+"""Sliding-window attention on the GPU against the fp64 definition in
+oracle/window.py.
+
+Tolerances. Rounding to bf16 is off by at most u = 2^-8 of the value. Scores are
+fp32 sums of d products: off by at most d 2^-24 scale |q||k|, and |q||k| stays below
+d + 9 sqrt(2 d) for d normal values a row (below 300 at d = 128): under
+128 * 2^-24 * 300 / sqrt(128) = 2.1e-4 of exponent; the exponential adds 2^-22. So a
+weight is within w = 2^-11 of itself before its rounding, and the log-sum-exp
+within 3e-4.
+  O: u |O| + (u + w) sum p |v|.
+"""
+import math
+
+import pytest
+import torch
+
+import chunk_routed_sparse_b200 as moc
+import oracle.window as W
+
+pytestmark = pytest.mark.gpu
+U, WT = 2.0 ** -8, 2.0 ** -11
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    yield
+    moc.check_window_error()
+
+
+def _rand(*shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def _qkv(B, Hq, Hk, Lq, Lk, d, seed=0):
+    return _rand(B, Hq, Lq, d, seed=seed), _rand(B, Hk, Lk, d, seed=seed + 1), _rand(B, Hk, Lk, d, seed=seed + 2)
+
+
+def _lens(x):
+    return None if x is None else torch.tensor(x, device="cuda", dtype=torch.int32)
+
+
+def _check_fwd(O, lse, ref):
+    assert torch.equal(torch.isinf(lse), torch.isinf(ref["lse"]))
+    fin = torch.isfinite(ref["lse"])
+    assert (lse.double() - ref["lse"])[fin].abs().max() <= 3e-4 if fin.any() else True
+    tol = U * ref["O"].abs() + (U + WT) * ref["sO"]
+    err = (O.double() - ref["O"]).abs()
+    assert (err <= tol).all(), float((err - tol).max())
+
+
+CASES = [  # B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len
+    (1, 1, 1, 1, 1, 64, -1, -1, 0, False, None, None),
+    (1, 1, 1, 1, 1, 128, 0, 0, 0, True, None, None),
+    (1, 2, 2, 300, 300, 64, 40, 7, 5, False, None, None),
+    (1, 2, 1, 257, 257, 128, 0, 0, 0, True, None, None),
+    (2, 4, 2, 513, 513, 64, 100, 0, 3, True, None, None),
+    (1, 2, 2, 700, 700, 128, 129, 129, 200, False, None, None),
+    (1, 1, 1, 1100, 1100, 64, 10, 0, 131, True, None, None),      # sinks apart from the window
+    (1, 3, 1, 640, 640, 128, -1, 0, 0, True, None, None),
+    (1, 2, 2, 384, 384, 64, -1, -1, 0, False, None, None),
+    (2, 2, 1, 200, 900, 128, 300, 20, 64, False, None, None),     # last rows of a longer stream
+    (2, 2, 2, 130, 1025, 64, 200, 0, 9, True, None, None),
+    (1, 2, 2, 300, 100, 64, 20, 0, 4, True, None, None),          # more rows than keys: the first see nothing
+    (1, 2, 2, 300, 100, 128, 20, 30, 0, False, None, None),
+    (1, 2, 2, 300, 0, 64, -1, -1, 3, False, None, None),          # no keys
+    (4, 2, 1, 333, 333, 128, 50, 0, 2, True, [333, 0, 1, 200], [333, 0, 1, 200]),
+    (3, 2, 2, 333, 500, 64, 64, 64, 7, False, [333, 10, 256], [500, 3, 129]),
+    (2, 1, 1, 140, 140, 64, 30, 0, 500, True, [-5, 999], [999, 999]),  # lengths outside the tensors are clamped
+    (1, 1, 1, 2112, 2112, 64, 256, 256, 64, False, None, None),   # the tiny scene: captions and a frame either side
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_forward_matches_the_definition(case):
+    B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, ql, kl = case
+    Q, K, V = _qkv(B, Hq, Hk, Lq, Lk, d)
+    ql, kl = _lens(ql), _lens(kl)
+    O = torch.full_like(Q, 5.0)
+    lse = torch.full((B, Hq, Lq), 5.0, device="cuda")
+    moc.window_attention_fwd(Q, K, V, left, right, sinks, causal, ql, kl, O=O, lse=lse)
+    ref = W.attention(Q, K, V, left, right, sinks, causal, ql, kl)
+    for b in range(B):
+        m = Lq if ql is None else min(max(int(ql[b]), 0), Lq)
+        assert (O[b, :, m:] == 5).all() and (lse[b, :, m:] == 5).all()  # rows behind the last: as they were
+        O[b, :, m:], lse[b, :, m:] = 0, -math.inf
+    _check_fwd(O, lse, ref)
+    O2, lse2 = moc.window_attention_fwd(Q, K, V, left, right, sinks, causal, ql, kl)
+    assert torch.equal(O2, O) and torch.equal(lse2, lse)
+    moc.check_window_error()
+
+
+def test_garbage_past_the_lengths_is_not_read():
+    B, H, L, d = 2, 2, 400, 128
+    Q, K, V = _qkv(B, H, H, L, L, d)
+    n = _lens([170, 301])
+    want = moc.window_attention_fwd(Q, K, V, 60, 0, 4, True, n, n)
+    for bad in (math.nan, math.inf):
+        q, k, v = Q.clone(), K.clone(), V.clone()
+        for b in range(B):
+            for t in (q, k, v):
+                t[b, :, int(n[b]):] = bad
+        got = moc.window_attention_fwd(q, k, v, 60, 0, 4, True, n, n)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_large_scores_and_scale():
+    """Scores up to some thousands: the running maximum moves by far more than the
+    lazy rescale's 2^8 and the softmax is nearly one-hot."""
+    Q, K, V = _qkv(1, 1, 1, 300, 300, 64)
+    Q, K = Q * 16, K * 16
+    ref = W.attention(Q, K, V, 100, 100, 0, False, scale=1.0)
+    O, lse = moc.window_attention_fwd(Q, K, V, 100, 100, 0, False, scale=1.0)
+    # scores of size 16 * 16 * 8: fp32 sums within 64 * 2^-24 * 16 * 16 * 130 = 0.13 in the worst order;
+    # rows whose two largest scores are 8 apart have every other weight below e^-7.8
+    s = (Q.double() @ K.double().transpose(-1, -2))
+    s = s.masked_fill(~W.visible(300, 300, 100, 100, 0, False, "cuda"), -math.inf)
+    top = s.topk(2, -1).values
+    clear = (top[..., 0] - top[..., 1]) > 8
+    assert clear.float().mean() > 0.9
+    assert ((lse.double() - ref["lse"]).abs() <= 0.13 + 1e-6 * ref["lse"].abs()).all()
+    err = (O.double() - ref["O"]).abs()[clear]
+    assert (err <= 2 * U * 5 + 100 * math.exp(-7.8) * 0.13 * 10).all()
