@@ -87,6 +87,8 @@ SIGNATURES = {
     "moc_outer_route": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P]),
     "moc_route_masked": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P]),
     "moc_window_attention": (_I, [_I, _I, _I, _I64, _I64, _I, _P, _P, _P] + _WIN + [_P, _P, _P]),
+    "moc_window_attention_bwd_workspace_bytes": (_SZ, [_I, _I, _I, _I64, _I64, _I, _I64, _I64, _I64, _I]),
+    "moc_window_attention_bwd": (_I, [_I, _I, _I, _I64, _I64, _I] + [_P] * 6 + _WIN + [_P] * 4 + [_SZ, _P]),
     "moc_window_device_error": (_I, [_P, _P]),
     "moc_build_rope": (_I, [_P, _P]),
     "moc_rope_destroy": (None, [_P]),
@@ -480,4 +482,5 @@ def check_device_error(ws: torch.Tensor) -> int:
 
 from .rows import (QKNormRope, QKVNormRope, Rope, Rotary, qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_fwd,  # noqa: E402,F401
                    qkv_norm_rope, qkv_norm_rope_bwd, qkv_norm_rope_fwd, rotary, rotary_bwd, rotary_fwd)
-from .window import check_window_error, window_attention_fwd  # noqa: E402,F401
+from .window import (WindowAttention, check_window_error, window_attention, window_attention_bwd,  # noqa: E402,F401
+                     window_attention_fwd)

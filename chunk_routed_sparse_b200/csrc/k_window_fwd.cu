@@ -20,6 +20,8 @@
 // their scores become -inf and their V rows are zeroed in shared memory (0 x NaN).
 // Every wait is bounded (2 s): a wait that gives up records itself in the error
 // word of moc_window_device_error and every role leaves.
+#include <mutex>
+
 #include "common.cuh"
 #include "pipeline.cuh"
 #include "tmap.cuh"
@@ -27,8 +29,30 @@
 
 namespace moc {
 
-// error code and detail of the window kernels on this device
-__device__ int32_t g_window_err[4];
+namespace {
+
+__device__ int32_t g_window_err[64];  // error code and detail of the window kernels on this device
+
+constexpr int kMaxDevices = 64;
+int32_t* g_err_ptr[kMaxDevices];
+cudaError_t g_err_status[kMaxDevices];
+std::once_flag g_err_once[kMaxDevices];
+
+}  // namespace
+
+cudaError_t window_error_word(int32_t** word) {
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(g_err_once[dev], [dev] {
+        void* p = nullptr;
+        g_err_status[dev] = cudaGetSymbolAddress(&p, g_window_err);
+        g_err_ptr[dev] = static_cast<int32_t*>(p);
+    });
+    *word = g_err_ptr[dev];
+    return g_err_status[dev];
+}
 
 namespace {
 
@@ -135,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sQ = base + C::oQ, sK = base + C::oK, sV = base + C::oV, sBar = base + C::oBar;
     Shared& sh = *reinterpret_cast<Shared*>(gbase + C::oBar + 160);
     volatile int* abort = &sh.abort;
-    int32_t* hdr = g_window_err;
+    int32_t* const hdr = g_window_err;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -496,18 +520,3 @@ cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void
 }
 
 }  // namespace moc
-
-extern "C" moc_status moc_window_device_error(int32_t* detail, moc_stream_t stream) {
-    int32_t h[2] = {0, 0};
-    cudaStream_t s = (cudaStream_t)stream;
-    if (cudaMemcpyFromSymbolAsync(h, moc::g_window_err, sizeof h, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return MOC_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return MOC_ERR_CUDA;
-    if (detail) *detail = h[0] != moc::ERR_NONE ? h[1] : 0;
-    if (h[0] == moc::ERR_NONE) return MOC_OK;
-    const int32_t zero[2] = {0, 0};
-    if (cudaMemcpyToSymbolAsync(moc::g_window_err, zero, sizeof zero, 0, cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return MOC_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return MOC_ERR_CUDA;
-    return h[0] == moc::ERR_TIMEOUT ? MOC_ERR_DEVICE_TIMEOUT : MOC_ERR_DEVICE_CHECK;
-}

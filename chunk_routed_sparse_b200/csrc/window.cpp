@@ -10,7 +10,7 @@ moc_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOC_OK : MOC_E
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-constexpr int64_t kMaxLen = int64_t(1) << 29;   // positions and their sums with a limit stay in 32 bits
+constexpr int64_t kMaxLen = int64_t(1) << 28;   // positions and their differences with a limit of 2^30 fit 32 bits
 constexpr int64_t kMaxRows = int64_t(1) << 31;  // rows of one tensor: a copy's row coordinate is 32 bits
 
 moc_status make_args(moc::WinArgs& a, int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, int64_t left,
@@ -53,4 +53,41 @@ extern "C" moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, in
     if (!aligned16(Q) || !aligned16(O) || (Lk > 0 && (!aligned16(K) || !aligned16(V))) || !aligned4(lse))
         return MOC_ERR_INVALID_ARG;
     return cuda_status(moc::launch_window_fwd(a, d, Q, K, V, O, lse, (cudaStream_t)stream));
+}
+
+extern "C" moc_status moc_window_device_error(int32_t* detail, moc_stream_t stream) {
+    int32_t* word = nullptr;
+    if (moc::window_error_word(&word) != cudaSuccess || !word) return MOC_ERR_CUDA;
+    return moc_check_device_error(word, 64 * sizeof(int32_t), detail, stream);
+}
+
+extern "C" size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d,
+                                                           int64_t left, int64_t right, int64_t sinks, int causal) {
+    moc::WinArgs a{};
+    if (make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, nullptr, nullptr, 1.f) != MOC_OK) return 0;
+    return moc::plan_window_bwd(a, d).total;
+}
+
+extern "C" moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
+                                               const void* K, const void* V, const void* O, const float* lse,
+                                               const void* dO, int64_t left, int64_t right, int64_t sinks, int causal,
+                                               const int32_t* q_len, const int32_t* kv_len, float softmax_scale,
+                                               void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
+                                               moc_stream_t stream) {
+    moc::WinArgs a{};
+    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len, softmax_scale);
+    if (st != MOC_OK) return st;
+    if (B == 0 || Hq == 0 || (Lq == 0 && Lk == 0)) return MOC_OK;
+    if (Lq > 0)
+        for (const void* t : {Q, O, dO, static_cast<const void*>(dQ)})
+            if (!aligned16(t)) return MOC_ERR_INVALID_ARG;
+    if (Lk > 0)
+        for (const void* t : {K, V, static_cast<const void*>(dK), static_cast<const void*>(dV)})
+            if (!aligned16(t)) return MOC_ERR_INVALID_ARG;
+    if ((Lq > 0 && !lse) || !aligned4(lse)) return MOC_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOC_ERR_INVALID_ARG;
+    const moc::WinBwdPlan p = moc::plan_window_bwd(a, d);
+    if (ws_bytes < p.total) return MOC_ERR_WORKSPACE_TOO_SMALL;
+    return cuda_status(moc::launch_window_bwd(a, d, Q, K, V, O, lse, dO, dQ, dK, dV, static_cast<char*>(ws), p,
+                                              (cudaStream_t)stream));
 }

@@ -107,6 +107,24 @@ __device__ __forceinline__ uint32_t bits(int lo, int hi) {
 }  // namespace win
 #endif
 
+// The window kernels' error code and detail on the current device (device memory).
+cudaError_t window_error_word(int32_t** word);
+
+// Workspace of the backward pass.
+struct WinBwdPlan {
+    size_t work = 0;     // int32[64]: work counters of the dQ and the dK / dV kernel
+    size_t dsum = 0;     // fp32 [B Hq Lq]: D = dO . o
+    size_t part = 0;     // fp32 [units][2][128][d]: dV, dK parts of the split key tiles
+    size_t total = 0;
+    int key_tiles = 0;   // of one (b, key head)
+    int split_tiles = 0; // leading key tiles whose rows are split over units
+    int splits = 1;      // units of such a tile
+};
+WinBwdPlan plan_window_bwd(const WinArgs& a, int d);
+cudaError_t launch_window_bwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, const void* O,
+                              const float* lse, const void* dO, void* dQ, void* dK, void* dV, char* ws,
+                              const WinBwdPlan& p, cudaStream_t s);
+
 cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
                               float* lse, cudaStream_t s);
 

@@ -18,6 +18,7 @@ import math
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check, _ptr, _stream, lib
 from .rows import _on
@@ -72,6 +73,69 @@ def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 
                                           1 if causal else 0, _ptr(q_len), _ptr(kv_len), float(scale), _ptr(O),
                                           _ptr(lse), _stream()), "moc_window_attention")
     return O, lse
+
+
+def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, sinks: int = 0, causal: bool = False,
+                         q_len: Optional[torch.Tensor] = None, kv_len: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, dQ: Optional[torch.Tensor] = None,
+                         dK: Optional[torch.Tensor] = None, dV: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None):
+    """(dQ, dK, dV) for the upstream gradient dO (moc_window_attention_bwd). Rows past
+    the lengths are left as they were in given tensors and are 0 in new ones."""
+    B, Hq, Hk, Lq, Lk, d = _problem(Q, K, V, q_len, kv_len)
+    _tensor("O", O, Q.shape, Q.device)
+    _tensor("dO", dO, Q.shape, Q.device)
+    _tensor("lse", lse, (B, Hq, Lq), Q.device, torch.float32)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    for name, x, ref in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, K)):
+        if x is not None:
+            _tensor(name, x, ref.shape, Q.device)
+    dQ = (torch.empty_like(Q) if q_len is None else torch.zeros_like(Q)) if dQ is None else dQ
+    dK = (torch.empty_like(K) if kv_len is None else torch.zeros_like(K)) if dK is None else dK
+    dV = (torch.empty_like(K) if kv_len is None else torch.zeros_like(K)) if dV is None else dV
+    with _on(Q.device):
+        if ws is None:
+            n = int(lib().moc_window_attention_bwd_workspace_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks,
+                                                                   1 if causal else 0))
+            if n == 0:
+                raise ValueError("invalid problem for the backward workspace size query")
+            ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+        elif ws.device != Q.device or not ws.is_contiguous():
+            raise ValueError(f"ws: expected a contiguous tensor on {Q.device}")
+        _check(lib().moc_window_attention_bwd(B, Hq, Hk, Lq, Lk, d, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
+                                              _ptr(dO), left, right, sinks, 1 if causal else 0, _ptr(q_len),
+                                              _ptr(kv_len), float(scale), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws),
+                                              ws.numel() * ws.element_size(), _stream()), "moc_window_attention_bwd")
+    return dQ, dK, dV
+
+
+class WindowAttention(torch.autograd.Function):
+    """window_attention_fwd with its gradient for Q, K and V.
+    apply(Q, K, V, left, right, sinks, causal, q_len, kv_len, scale) -> O."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, left, right, sinks, causal, q_len, kv_len, scale):
+        Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+        O, lse = window_attention_fwd(Q, K, V, left, right, sinks, causal, q_len, kv_len, scale)
+        ctx.args = (left, right, sinks, causal, scale)
+        ctx.save_for_backward(Q, K, V, O, lse, q_len, kv_len)
+        return O
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, O, lse, q_len, kv_len = ctx.saved_tensors
+        left, right, sinks, causal, scale = ctx.args
+        grads = window_attention_bwd(Q, K, V, O, lse, dO.contiguous().to(torch.bfloat16), left, right, sinks, causal,
+                                     q_len, kv_len, scale)
+        return (*grads, None, None, None, None, None, None, None)
+
+
+def window_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, left: int = -1, right: int = -1, sinks: int = 0,
+                     causal: bool = False, q_len: Optional[torch.Tensor] = None,
+                     kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None) -> torch.Tensor:
+    """Differentiable sliding-window attention: bf16 O [B, Hq, Lq, d] (0 past q_len)."""
+    return WindowAttention.apply(Q, K, V, left, right, sinks, causal, q_len, kv_len, scale)
 
 
 def check_window_error() -> int:

@@ -8,6 +8,15 @@ d + 9 sqrt(2 d) for d normal values a row (below 300 at d = 128): under
 weight is within w = 2^-11 of itself before its rounding, and the log-sum-exp
 within 3e-4.
   O: u |O| + (u + w) sum p |v|.
+  dQ, dK, dV: u of the value, and u + w of the terms (oracle: sQ, sK, sV) for the
+    rounding of ds or p before the last product. ds = p (dO . v - D) goes by what it is
+    a difference of: dO . v is an fp32 sum of d products (within d 2^-24 of |dO||v|) and
+    D = dO . O has O rounded by u (and its weights, u + w), so up to (2 u + w) sum
+    |dO||O| of D's terms: the oracle's sizes hold |dO| . |v| for the one and, as
+    |O| <= sum p |v|, an average of such for the other, which the shared size stands for
+    over a row. In all u |x| + (4 u + 2 w) size for dQ and dK, u |x| + (u + w) size for
+    dV; and, the errors being many, independent and mostly far smaller, 2 u in the
+    2-norm over a batch entry (a rounding's own share is u / sqrt(3)).
 """
 import math
 
@@ -123,3 +132,119 @@ def test_large_scores_and_scale():
     assert ((lse.double() - ref["lse"]).abs() <= 0.13 + 1e-6 * ref["lse"].abs()).all()
     err = (O.double() - ref["O"]).abs()[clear]
     assert (err <= 2 * U * 5 + 100 * math.exp(-7.8) * 0.13 * 10).all()
+
+
+def _check_bwd(got, ref, ql, kl, Lq, Lk):
+    for name, size, k, lens, L in (("dQ", "sQ", 4 * U + 2 * WT, ql, Lq), ("dK", "sK", 4 * U + 2 * WT, kl, Lk),
+                                   ("dV", "sV", U + WT, kl, Lk)):
+        x, want = got[name].double(), ref[name]
+        for b in range(x.shape[0]):
+            n = L if lens is None else min(max(int(lens[b]), 0), L)
+            err = (x[b, :, :n] - want[b, :, :n]).abs()
+            tol = U * want[b, :, :n].abs() + k * ref[size][b, :, :n] + 1e-30
+            assert (err <= tol).all(), (name, b, float((err - tol).max()))
+            if n and want[b].abs().max() > 0 and want[b, :, :n].numel() > 1000:
+                rel = (err.square().sum() / want[b, :, :n].square().sum()).sqrt()
+                assert rel <= 2 * U, (name, b, float(rel))
+            if lens is not None:
+                assert (x[b, :, n:] == 5).all(), name  # as they were
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_gradient_matches_the_definition(case):
+    B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, ql, kl = case
+    Q, K, V = _qkv(B, Hq, Hk, Lq, Lk, d)
+    g = _rand(B, Hq, Lq, d, seed=9)
+    ql, kl = _lens(ql), _lens(kl)
+    args = (left, right, sinks, causal, ql, kl)
+    O, lse = moc.window_attention_fwd(Q, K, V, *args)
+    ref = W.attention(Q, K, V, *args, dO=g)
+    got = {n: torch.full_like(t, 5.0) for n, t in (("dQ", Q), ("dK", K), ("dV", V))}
+    moc.window_attention_bwd(Q, K, V, O, lse, g, *args, **got)
+    moc.check_window_error()
+    _check_bwd(got, ref, ql, kl, Lq, Lk)
+
+
+def test_gradients_with_shared_first_keys_split_over_many_rows():
+    """First keys seen by thousands of rows of six query heads: their tiles' rows are
+    split over units and joined."""
+    B, Hq, Hk, L, d = 1, 6, 2, 3333, 64
+    Q, K, V = _qkv(B, Hq, Hk, L, L, d)
+    g = _rand(B, Hq, L, d, seed=9)
+    args = (60, 0, 150, True)
+    O, lse = moc.window_attention_fwd(Q, K, V, *args)
+    got = dict(zip(("dQ", "dK", "dV"), moc.window_attention_bwd(Q, K, V, O, lse, g, *args)))
+    _check_bwd(got, W.attention(Q, K, V, *args, dO=g), None, None, L, L)
+    again = moc.window_attention_bwd(Q, K, V, O, lse, g, *args)
+    for a, b in zip(got.values(), again):
+        assert torch.equal(a, b)
+
+
+def test_gradient_ignores_garbage_past_the_lengths():
+    B, H, L, d = 2, 2, 400, 128
+    Q, K, V = _qkv(B, H, H, L, L, d)
+    g = _rand(B, H, L, d, seed=9)
+    n = _lens([170, 301])
+    args = (60, 0, 4, True, n, n)
+    O, lse = moc.window_attention_fwd(Q, K, V, *args)
+    want = moc.window_attention_bwd(Q, K, V, O, lse, g, *args)
+    for bad in (math.nan, math.inf):
+        t = [x.clone() for x in (Q, K, V, O, g)]
+        l2 = lse.clone()
+        for b in range(B):
+            for x in t:
+                x[b, :, int(n[b]):] = bad
+            l2[b, :, int(n[b]):] = bad
+        for a, b in zip(moc.window_attention_bwd(*t[:4], l2, t[4], *args), want):
+            assert torch.equal(a, b)
+
+
+def test_gradient_against_differences():
+    """<grad, v> against central differences of the definition's sum(dO * O) in fp64 along
+    v = grad / |grad| (h = 1e-4: truncation and rounding below 1e-6 of it). The gradient is
+    within 2 u of itself in the 2-norm, so is its product with a unit vector
+    (Cauchy-Schwarz)."""
+    Q, K, V = _qkv(1, 2, 1, 96, 96, 64)
+    g = _rand(1, 2, 96, 64, seed=9)
+    args = (30, 0, 4, True)
+    O, lse = moc.window_attention_fwd(Q, K, V, *args)
+    grads = moc.window_attention_bwd(Q, K, V, O, lse, g, *args)
+    x = [t.double() for t in (Q, K, V)]
+    for i in range(3):
+        v = grads[i].double() / grads[i].double().norm()
+        f = []
+        for h in (1e-4, -1e-4):
+            y = list(x)
+            y[i] = x[i] + h * v
+            f.append((g.double() * W.attention(*y, *args)["O"]).sum())
+        want = float(f[0] - f[1]) / 2e-4
+        assert abs(float((grads[i].double() * v).sum()) - want) <= (2 * U + 1e-6) * want
+
+
+def test_autograd_and_capture():
+    B, Hq, Hk, L, d = 2, 4, 2, 700, 64
+    Q, K, V = (x.requires_grad_() for x in _qkv(B, Hq, Hk, L, L, d))
+    n = _lens([700, 123])
+    O = moc.window_attention(Q, K, V, 200, 0, 16, True, n, n)
+    assert (O[1, :, 123:] == 0).all()
+    g = _rand(B, Hq, L, d, seed=3)
+    O.backward(g)
+    q, k, v = (x.detach() for x in (Q, K, V))
+    args = (200, 0, 16, True, n, n)
+    o, lse = moc.window_attention_fwd(q, k, v, *args)
+    want = moc.window_attention_bwd(q, k, v, o, lse, g, *args)
+    for x, w in zip((Q, K, V), want):
+        assert torch.equal(x.grad, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = moc.window_attention_fwd(q, k, v, *args)
+        grads = moc.window_attention_bwd(q, k, v, *held, g, *args)
+    for _ in range(2):
+        for t in (*held, *grads):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held[0], o)
+        for a, b in zip(grads, want):
+            assert torch.equal(a, b)
+    moc.check_window_error()
