@@ -8,12 +8,19 @@
 // rounded to bf16 (2^-8 of each) as operands of the last products; all sums are in
 // fp32.
 //
-// Three launches: D (which also clears the work counters), dQ (a work unit is a
-// 128-row tile, it owns its dQ rows) and dK / dV (a unit is a 128-key tile of a key
-// head, it owns its dK and dV rows and walks the rows that see it). The first keys
-// are seen by every later row: their tiles' rows are split over units that write
-// fp32 parts, added in order by a fourth launch. No atomics on results: they do not
-// depend on the order of the units, which are handed out longest first by a counter.
+// Launches: one that forms each row's statistics (the log-sum-exp in exp2 units and
+// D) and clears the work counters; dQ (a work unit is a 128-row tile, it owns its dQ
+// rows); dK / dV (a unit is a 128-key tile of a key head, it owns its dK and dV rows
+// and walks the rows that see it). The first keys are seen by every later row: their
+// tiles' rows are split over units that write fp32 parts, added in order by a fourth
+// launch. No atomics on results: they do not depend on the order of the units, which
+// are handed out longest first by a counter.
+//
+// D from the rounded O is off by what O's rounding carries, which a row of few keys
+// feels as much as the roundings of p and ds. As sum_u ds_tu = 0 for the exact D, the
+// dQ kernel adds the sum r of its unrounded ds to D for the dK / dV kernel, and walks
+// units of at most kProbeKeys keys twice, the first time for r alone (two of their
+// three products again; such units are short).
 #include "common.cuh"
 #include "pipeline.cuh"
 #include "tmap.cuh"
@@ -27,6 +34,12 @@ using win::kTile;
 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kProbeKeys = 384;
+
+// Row statistics (log2 sum exp2 of the scores, D), rows of a head padded to an even
+// count (16-byte copies of any even row) and 128 more at the end: +inf, 0 where there
+// is no row or the row sees no key, so that every p of it is zero.
+__device__ __forceinline__ int64_t stat_row(const WinArgs& a, int64_t head) { return head * ((a.Lq + 1) & ~1); }
 
 struct Shared {
     int item[2];
@@ -46,31 +59,38 @@ __device__ __forceinline__ void mask_cols(uint32_t addr, uint32_t keep, uint32_t
 }
 constexpr uint32_t kMinusInf = 0xff800000u;
 
-// ---- D -------------------------------------------------------------------------
+// ---- row statistics ------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(256) window_rowdot_kernel(const __grid_constant__ WinArgs a,
-                                                            const __nv_bfloat16* __restrict__ O,
-                                                            const __nv_bfloat16* __restrict__ dO,
-                                                            float* __restrict__ Dsum, int32_t* __restrict__ work) {
-    constexpr int LPR = D / 8;  // lanes a row, 16 bytes each
+__global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant__ WinArgs a,
+                                                           const __nv_bfloat16* __restrict__ O,
+                                                           const __nv_bfloat16* __restrict__ dO,
+                                                           const float* __restrict__ lse, float2* __restrict__ stats,
+                                                           int32_t* __restrict__ work) {
+    constexpr int LPR = D / 8, RPC = 256 / LPR;  // lanes a row (16 bytes each), rows a step
     if (blockIdx.x == 0 && threadIdx.x < 2) work[threadIdx.x] = 0;
-    const int64_t rows = int64_t(a.B) * a.Hq * a.Lq;
+    const int per = (a.Lq + 1) & ~1;
+    const int64_t heads = int64_t(a.B) * a.Hq, total = heads * per + 128;
     const int r = threadIdx.x % LPR;
-    for (int64_t row0 = int64_t(blockIdx.x) * (256 / LPR); row0 < rows; row0 += int64_t(gridDim.x) * (256 / LPR)) {
-        const int64_t row = row0 + threadIdx.x / LPR;
-        float acc = 0.f;
-        if (row < rows) {
-            const uint4 x = ldg_nc16(O + size_t(row) * D + r * 8), y = ldg_nc16(dO + size_t(row) * D + r * 8);
+    for (int64_t i0 = int64_t(blockIdx.x) * RPC; i0 < total; i0 += int64_t(gridDim.x) * RPC) {
+        const int64_t i = i0 + threadIdx.x / LPR;
+        const int64_t head = per > 0 ? i / per : heads;
+        const int t = int(i - head * per);
+        float acc = 0.f, l2 = INFINITY;
+        if (head < heads && t < win::seq(a, int(head / a.Hq)).m) {
+            const size_t row = size_t(head) * a.Lq + t;
+            const uint4 x = ldg_nc16(O + row * D + r * 8), y = ldg_nc16(dO + row * D + r * 8);
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc = fmaf(bf16lo(xs[i]), bf16lo(ys[i]), acc);
-                acc = fmaf(bf16hi(xs[i]), bf16hi(ys[i]), acc);
+            for (int k = 0; k < 4; ++k) {
+                acc = fmaf(bf16lo(xs[k]), bf16lo(ys[k]), acc);
+                acc = fmaf(bf16hi(xs[k]), bf16hi(ys[k]), acc);
             }
+            const float v = __ldg(lse + row);
+            if (v > -INFINITY || v != v) l2 = v * kLog2e;
         }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o, LPR);
-        if (r == 0 && row < rows) Dsum[row] = acc;
+        if (r == 0 && i < total) stats[i] = make_float2(l2, l2 == INFINITY ? 0.f : acc);
     }
 }
 
@@ -98,8 +118,11 @@ struct Cfg {
     static constexpr int oDO = oQ + kTileBytes;
     static constexpr int oK = oDO + kTileBytes;      // 3 stages
     static constexpr int oV = oK + 3 * kTileBytes;   // 2 stages
-    static constexpr int oBar = oV + 2 * kTileBytes;
-    static constexpr int kSmem = (oBar + 512 + 1024) > 120 * 1024 ? (oBar + 512 + 1024) : 120 * 1024;
+    static constexpr int oSum = oV + 2 * kTileBytes;  // fp32 [2 exchanges][2 warpgroups][128]
+    static constexpr int oBar = oSum + 2048;
+    // the dynamic shared memory of a kernel without static shared memory starts on a
+    // 1024-byte boundary (checked at the start): no room for slack at d = 128
+    static constexpr int kSmem = oBar + 256 > 120 * 1024 ? oBar + 256 : 120 * 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0);
     static constexpr uint32_t kIdescDQ = idesc_bf16_f32(128, D, 1);
@@ -107,15 +130,18 @@ struct Cfg {
 
 enum {
     B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 7, B_V_FULL = 10, B_V_EMPTY = 12, B_QDO_FULL = 14,
-    B_QDO_EMPTY = 15, B_S_FULL = 16, B_DP_FULL = 18, B_DS_FULL = 19, B_DQ_DONE = 20, B_MMA_DONE = 21, B_COUNT = 22
+    B_QDO_EMPTY = 15, B_S_FULL = 16, B_DP_FULL = 18, B_DS_FULL = 19, B_DQ_DONE = 20, B_MMA_DONE = 21, B_SUM = 22, B_COUNT = 23
 };
+static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 
 __device__ __forceinline__ uint32_t col_s(int b) { return b ? kColS1 : kColS0; }
 // column (from a buffer's first) of the bf16 pairs of keys 16 kk .. + 15
 __device__ __forceinline__ uint32_t ds_col(int kk) { return 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3); }
 
 struct Unit {
-    int b, hq, t0, rows, tiles;
+    int b, hq, t0, rows;
+    int tiles;  // key tiles
+    int probe;  // tiles walked first for the sum of ds alone: `tiles` or 0
     win::Seq seq;
     win::Span y;
 };
@@ -131,23 +157,26 @@ __device__ __forceinline__ void decode(const WinArgs& a, int nqt, int u, Unit& x
     x.y = win::Span{0, 0, 0, 0, 0};
     if (x.rows > 0) x.y = win::span(a, x.seq, x.t0, x.t0 + x.rows);
     x.tiles = x.y.na + x.y.nb;
+    x.probe = x.y.a1 + x.y.b1 - x.y.b0 <= kProbeKeys ? x.tiles : 0;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ WinArgs a, int n_units, int nqt, const float* __restrict__ lse,
-                     const float* __restrict__ Dsum, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
+                     const __grid_constant__ WinArgs a, int n_units, int nqt, float2* __restrict__ stats,
+                     int32_t* __restrict__ work, int32_t* __restrict__ hdr,
                      __nv_bfloat16* __restrict__ dQ) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    unsigned char* gbase = smem_raw + (base - raw);
+    const uint32_t base = smem_u32(smem_raw);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) set_error(hdr, ERR_CHECK, 230);
+        return;
+    }
     const uint32_t sQ = base + C::oQ, sDO = base + C::oDO, sK = base + C::oK, sV = base + C::oV;
     const uint32_t sBar = base + C::oBar;
-    Shared& sh = *reinterpret_cast<Shared*>(gbase + C::oBar + 256);
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + C::oBar + 8 * B_COUNT);
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -156,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < B_COUNT; ++x) {
             int n = 1;
             if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256;
-            if (x == B_DS_FULL) n = 256;
+            if (x == B_DS_FULL || x == B_SUM) n = 256;
             mbar_init(bar(x), n);
         }
         sh.abort = 0;
@@ -201,9 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(sQ + s * C::kSlabBytes, &tmQ, bar(B_QDO_FULL), 64 * s, qrow);
                     tma_load_2d(sDO + s * C::kSlabBytes, &tmDO, bar(B_QDO_FULL), 64 * s, qrow);
                 }
-                for (int j = 0; j < x.tiles; ++j) {
+                for (int j = 0; j < x.probe + x.tiles; ++j) {
                     int key0, end;
-                    win::tile(x.y, j, key0, end);
+                    win::tile(x.y, j < x.probe ? j : j - x.probe, key0, end);
                     const uint32_t ks = gk % 3, vs = gv & 1;
                     if (!wait_bar(bar(B_K_EMPTY + ks), ((gk / 3) & 1) ^ 1, abort, hdr, 233)) { stop = true; break; }
                     mbar_expect_tx(bar(B_K_FULL + ks), C::kTileBytes);
@@ -265,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (u < 0) break;
                 Unit x;
                 decode(a, nqt, u, x);
-                const int T = x.tiles;
+                const int T = x.probe + x.tiles;
                 if (T == 0) continue;
                 if (!wait_bar(bar(B_QDO_FULL), nu & 1, abort, hdr, 244)) break;
                 ++nu;
@@ -279,10 +308,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 < T && !issue_dp()) { stop = true; break; }
                     if (T > 1 && j == T - 2) umma_commit(bar(B_QDO_EMPTY));  // the last S was issued before it
                     const uint32_t ks = (gk + j) % 3, kb = sK + ks * C::kTileBytes;
+                    if (j >= x.probe) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(tmem + kColDQ, tmem + col_s(j & 1) + ds_col(kk),
-                                sdesc_sw128(kb + kk * 2048, C::kSlabBytes, 1024), C::kIdescDQ, (j > 0 || kk > 0));
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_ts(tmem + kColDQ, tmem + col_s(j & 1) + ds_col(kk),
+                                    sdesc_sw128(kb + kk * 2048, C::kSlabBytes, 1024), C::kIdescDQ, (j > x.probe || kk > 0));
+                    }
                     umma_commit(bar(B_K_EMPTY + ks));
                     if (j + 2 < T && !issue_s(gk + j + 2, j & 1)) { stop = true; break; }
                 }
@@ -300,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wg = warp >> 2, row = tid & 127;
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
         const float sl2 = a.scale * kLog2e;
-        uint32_t gt = 0, nu = 0, ns[2] = {0, 0}, gk = 0;
+        uint32_t gt = 0, nu = 0, ns[2] = {0, 0}, gk = 0, nx = 0;
         for (int it = 0;; ++it) {
             const int slot = it & 1;
             if (!wait_bar_warp(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 251)) break;
@@ -312,18 +343,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.rows <= 0) continue;
             const bool live = row < x.rows;
             const size_t rowg = (size_t(x.b) * a.Hq + x.hq) * size_t(a.Lq) + size_t(x.t0) + row;
-            // rows past the last, and rows that see no key (lse = -inf): +inf makes every p zero
-            float lse2 = INFINITY, drow = 0.f;
-            if (live) {
-                const float v = __ldg(lse + rowg);
-                if (v > -INFINITY || v != v) lse2 = v * kLog2e;
-                drow = __ldg(Dsum + rowg);
-            }
+            float2* my = stats + stat_row(a, int64_t(x.b) * a.Hq + x.hq) + x.t0 + row;
+            const float2 st = live ? *my : make_float2(INFINITY, 0.f);
+            const float lse2 = st.x;
+            float drow = st.y;
+            // adds to drow what the two warpgroups have for their halves of the row's keys;
+            // exchanges alternate between two buffers, so that one's values are read before
+            // the next but one overwrites them
+            auto add_both = [&](float v) -> bool {
+                float* sums = reinterpret_cast<float*>(smem_raw + C::oSum) + (nx & 1) * 256;
+                sums[wg * 128 + row] = v;
+                mbar_arrive(bar(B_SUM));
+                if (!wait_bar_warp(bar(B_SUM), nx & 1, abort, hdr, 255)) return false;
+                ++nx;
+                drow += sums[row] + sums[128 + row];
+                return true;
+            };
+            uint64_t ra = 0, rb = 0;  // packed sums of the unrounded ds
+            auto half_sum = [&]() -> float {
+                float r0, r1, r2, r3;
+                f2_unpack(ra, r0, r1);
+                f2_unpack(rb, r2, r3);
+                ra = rb = 0;
+                return (r0 + r1) + (r2 + r3);
+            };
             const win::Row vis = win::row(a, x.seq.n, x.t0 + row + x.seq.shift);
             bool stop = false;
-            for (int j = 0; j < x.tiles; ++j, ++gk) {
+            for (int j = 0; j < x.probe + x.tiles; ++j, ++gk) {
                 int key0, end;
-                win::tile(x.y, j, key0, end);
+                win::tile(x.y, j < x.probe ? j : j - x.probe, key0, end);
+                if (j > 0 && j == x.probe && !add_both(half_sum())) { stop = true; break; }
                 const int b = j & 1;
                 if (!wait_bar_warp(bar(B_S_FULL + b), (b ? ns[1] : ns[0]) & 1, abort, hdr, 252)) { stop = true; break; }
                 if (b) ++ns[1]; else ++ns[0];
@@ -354,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 32; ++c) {
                     const float d0 = ex2(fmaf(__uint_as_float(s[2 * c]), sl2, -lse2)) * (__uint_as_float(p[2 * c]) - drow);
                     const float d1 = ex2(fmaf(__uint_as_float(s[2 * c + 1]), sl2, -lse2)) * (__uint_as_float(p[2 * c + 1]) - drow);
+                    if (c & 1) rb = f2_add(rb, f2_pack(d0, d1));
+                    else ra = f2_add(ra, f2_pack(d0, d1));
                     pk[c] = pack_bf16(d0, d1);
                 }
                 tmem_st32(s_addr, pk);
@@ -375,6 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (stop) break;
             // dq_t = scale * accumulator; this warpgroup's half of the columns
             if (x.tiles > 0) {
+                if (!add_both(half_sum())) break;
+                if (wg == 0 && live && lse2 < INFINITY) *my = make_float2(lse2, drow);
                 if (!wait_bar_warp(bar(B_DQ_DONE), nu & 1, abort, hdr, 254)) break;
                 ++nu;
                 tc_fence_after();
@@ -416,21 +469,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace dq
 
 // ---- dK, dV --------------------------------------------------------------------
-// One CTA per SM, 512 threads. TMEM: S^T and dP^T (128 keys x 128 rows) and the dV
-// and dK accumulators.
-//   warp 12 (one lane): units and TMA of a unit's K and V tiles (loaded once the
-//          previous unit's last S^T and dP^T have read theirs).
-//   warps 8-11: copy each 128-row tile's Q and dO (16-byte pieces into the swizzled
-//          layout, zeros past the last row) and its lse and D into a 2-stage ring.
-//   warp 13 (one lane): S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and
-//          dK += dS^T Q with P^T and dS^T from TMEM.
-//   warps 0-7: two warpgroups, each 64 of the tile's rows for all 128 keys (one
-//          thread a key): P^T and dS^T as bf16 over its own halves of S^T and dP^T.
+// One CTA per SM, 384 threads, 128-row tiles. TMEM is full with S^T, dP^T (128 keys x
+// 128 rows) and the dV and dK accumulators, so nothing can be double-buffered; the
+// tensor core is kept busy by the order of its products instead:
+//     dV(i-1) S^T(i) | dK(i-1) dP^T(i) | dV(i) S^T(i+1) | ...
+// S^T(i) runs as soon as dV(i-1) has read P^T(i-1) in its columns, while ds(i-1) is
+// formed; the exponentials of tile i run under dK(i-1) and dP^T(i). (All four products
+// of a tile in a row, then its math: 2.80 ms on the single-shot training step against
+// 2.15 ms; two TMEM buffers of 64 rows each: 3.14 ms, a 64-column product takes as
+// long as a 128-column one.)
+//   warp 8 (one lane): units and TMA: K and V of a unit, Q tiles into a 3-stage ring,
+//          dO tiles and row statistics into a 2-stage ring.
+//   warp 9 (one lane): the products.
+//   warps 0-7: two warpgroups, each 64 of the tile's rows for all 128 keys (one thread
+//          a key): P^T, then dS^T, as bf16 over its own halves of S^T and dP^T.
 namespace dkv {
 
-constexpr int kThreads = 512;
-// launched at 128 registers a thread: 2 x 128 x 176 + 128 x 104 + 128 x 56 = 512 x 128
-constexpr int kRegsCompute = 176, kRegsGather = 104, kRegsOther = 56;
+constexpr int kThreads = 384;
+// launched at 168 registers a thread: 2 x 128 x 216 + 128 x 72 = 384 x 168
+constexpr int kRegsCompute = 216, kRegsOther = 72;
 constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 384;
 
 template <int D>
@@ -438,28 +495,34 @@ struct Cfg {
     static constexpr int kSlabs = D / 64;
     static constexpr int kSlabBytes = 128 * 128;
     static constexpr int kTileBytes = kSlabs * kSlabBytes;
+    static constexpr int kQStages = 3, kOStages = 2;
+    static constexpr int kStatBytes = kTile * 8;
     static constexpr int oK = 0;
     static constexpr int oV = oK + kTileBytes;
-    static constexpr int oQ = oV + kTileBytes;          // 2 stages
-    static constexpr int oDO = oQ + 2 * kTileBytes;     // 2 stages
-    static constexpr int oStat = oDO + 2 * kTileBytes;  // [2 stages][lse2 | D][128] fp32
-    static constexpr int oBar = oStat + 2 * 2 * 128 * 4;
-    static constexpr int kSmem = (oBar + 512 + 1024) > 120 * 1024 ? (oBar + 512 + 1024) : 120 * 1024;
+    static constexpr int oQ = oV + kTileBytes;
+    static constexpr int oDO = oQ + kQStages * kTileBytes;
+    static constexpr int oStat = oDO + kOStages * kTileBytes;  // [stage][row] (log-sum-exp, D)
+    static constexpr int oBar = oStat + kOStages * kStatBytes;
+    // the dynamic shared memory of a kernel without static shared memory starts on a
+    // 1024-byte boundary (checked at the start): no room for slack at d = 128
+    static constexpr int kSmem = oBar + 256 > 120 * 1024 ? oBar + 256 : 120 * 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0);
     static constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, 1);
 };
 
 enum {
-    B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_KV_FULL = 4, B_KV_EMPTY = 5, B_QT_FULL = 6, B_QT_EMPTY = 8, B_ST_FULL = 10,
-    B_P_FULL = 11, B_ACC_DONE = 12, B_MMA_DONE = 13, B_COUNT = 14
+    B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_KV_FULL = 4, B_KV_EMPTY = 5, B_Q_FULL = 6, B_Q_EMPTY = 9, B_O_FULL = 12,
+    B_O_EMPTY = 14, B_S_FULL = 16, B_P_FULL = 17, B_DP_FULL = 18, B_DS_FULL = 19, B_ACC_DONE = 20, B_EPI_DONE = 21,
+    B_MMA_DONE = 22, B_TAIL = 23, B_COUNT = 25
 };
+static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 
 // A unit: a key tile of a (batch, key head), all of its row tiles or one split of them.
 struct Unit {
     int b, hk, k0, nk;     // nk <= 0: no keys
     int t_lo, t_hi;        // rows of a query head that may see it
-    int per_head;          // their 128-row tiles
+    int per_head;          // their tiles
     int i0, i1;            // this unit's tiles, counted over the heads of the group
     int part;              // split: index of the fp32 part, else -1
     win::Seq seq;
@@ -489,7 +552,7 @@ __device__ __forceinline__ void decode(const WinArgs& a, const WinBwdPlan& p, in
     int p_lo = first ? -(1 << 30) : x.k0 - a.right;
     if (a.causal) p_lo = max(p_lo, x.k0);
     const int p_hi = first ? (1 << 30) : x.k0 + x.nk - 1 + a.left;  // last position
-    x.t_lo = max(p_lo - x.seq.shift, 0);
+    x.t_lo = max(p_lo - x.seq.shift, 0) & ~1;                       // even: 16-byte copies of the statistics
     x.t_hi = min(p_hi - x.seq.shift + 1, x.seq.m);
     if (x.t_hi <= x.t_lo) return;
     x.per_head = (x.t_hi - x.t_lo + kTile - 1) / kTile;
@@ -506,23 +569,29 @@ __device__ __forceinline__ void row_tile(const WinArgs& a, const Unit& x, int i,
     n = min(kTile, x.t_hi - t0);
 }
 
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                       const __grid_constant__ WinArgs a, const __grid_constant__ WinBwdPlan p, int n_units,
-                      const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ dO,
-                      const float* __restrict__ lse, const float* __restrict__ Dsum, int32_t* __restrict__ work,
-                      int32_t* __restrict__ hdr, float* __restrict__ parts, __nv_bfloat16* __restrict__ dK,
-                      __nv_bfloat16* __restrict__ dV) {
+                      const float2* __restrict__ stats, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
+                      float* __restrict__ parts, __nv_bfloat16* __restrict__ dK, __nv_bfloat16* __restrict__ dV) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    unsigned char* gbase = smem_raw + (base - raw);
+    const uint32_t base = smem_u32(smem_raw);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) set_error(hdr, ERR_CHECK, 260);
+        return;
+    }
     const uint32_t sK = base + C::oK, sV = base + C::oV, sQ = base + C::oQ, sDO = base + C::oDO;
-    float* stat = reinterpret_cast<float*>(gbase + C::oStat);  // [stage][0: lse2, 1: D][128]
     const uint32_t sBar = base + C::oBar;
-    Shared& sh = *reinterpret_cast<Shared*>(gbase + C::oBar + 256);
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + C::oBar + 8 * B_COUNT);
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -530,15 +599,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) {
             int n = 1;
-            if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256 + 128;
-            if (x == B_QT_FULL || x == B_QT_FULL + 1) n = 128;
-            if (x == B_P_FULL) n = 256;
+            if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256;
+            if (x == B_O_EMPTY || x == B_O_EMPTY + 1) n = 1 + 256;  // dV has read dO, the warps the statistics
+            if (x == B_P_FULL || x == B_DS_FULL || x == B_EPI_DONE) n = 256;
+            if (x == B_TAIL || x == B_TAIL + 1) n = 128;
             mbar_init(bar(x), n);
         }
         sh.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 13) {
+    if (warp == 9) {
         tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
         tmem_relinquish();
     }
@@ -547,14 +617,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
 
-    if (warp >= 12) {
+    if (warp >= 8) {
         regs_dec<kRegsOther>();
-        if (warp == 12 && lane == 0) {
-            // ---------------------------------------------------------- units + K/V loads
+        if (warp == 8 && lane == 0) {
+            // ---------------------------------------------------------- units + loads
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
-            uint32_t nu = 0;
-            for (int it = 0;; ++it) {
+            prefetch_tmap(&tmQ);
+            prefetch_tmap(&tmDO);
+            uint32_t nu = 0, g = 0;  // units with tiles, tiles
+            bool stop = false;
+            for (int it = 0; !stop; ++it) {
                 const int slot = it & 1;
                 if (!wait_bar(bar(B_ITEM_EMPTY + slot), ((it >> 1) & 1) ^ 1, abort, hdr, 261)) break;
                 const int u = atomicAdd(work, 1);
@@ -573,123 +646,114 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(sK + s * C::kSlabBytes, &tmK, bar(B_KV_FULL), 64 * s, krow);
                     tma_load_2d(sV + s * C::kSlabBytes, &tmV, bar(B_KV_FULL), 64 * s, krow);
                 }
+                for (int i = x.i0; i < x.i1; ++i, ++g) {
+                    int hq, t0, n;
+                    row_tile(a, x, i, hq, t0, n);
+                    const int64_t head = int64_t(x.b) * a.Hq + hq;
+                    const int qrow = int(head * a.Lq) + t0;
+                    const uint32_t qs = g % 3, os = g & 1;
+                    if (!wait_bar(bar(B_Q_EMPTY + qs), ((g / 3) & 1) ^ 1, abort, hdr, 263)) { stop = true; break; }
+                    mbar_expect_tx(bar(B_Q_FULL + qs), C::kTileBytes);
+#pragma unroll
+                    for (int s = 0; s < C::kSlabs; ++s)
+                        tma_load_2d(sQ + qs * C::kTileBytes + s * C::kSlabBytes, &tmQ, bar(B_Q_FULL + qs), 64 * s, qrow);
+                    if (!wait_bar(bar(B_O_EMPTY + os), ((g >> 1) & 1) ^ 1, abort, hdr, 264)) { stop = true; ++g; break; }
+                    mbar_expect_tx(bar(B_O_FULL + os), C::kTileBytes + C::kStatBytes);
+#pragma unroll
+                    for (int s = 0; s < C::kSlabs; ++s)
+                        tma_load_2d(sDO + os * C::kTileBytes + s * C::kSlabBytes, &tmDO, bar(B_O_FULL + os), 64 * s, qrow);
+                    bulk_load(base + C::oStat + os * C::kStatBytes, stats + stat_row(a, head) + t0, C::kStatBytes,
+                              bar(B_O_FULL + os));
+                }
             }
-            if (nu > 0) drain_bar(bar(B_KV_FULL), (nu - 1) & 1, hdr, 263);
-        } else if (warp == 13 && lane == 0) {
+            // every issued copy lands before the CTA exits (after an abort the last dO copy may
+            // not have been issued: its wait then runs out)
+            if (nu > 0) drain_bar(bar(B_KV_FULL), (nu - 1) & 1, hdr, 265);
+            for (uint32_t i = g >= 3 ? g - 3 : 0; i < g; ++i) drain_bar(bar(B_Q_FULL + i % 3), (i / 3) & 1, hdr, 266);
+            for (uint32_t i = g >= 2 ? g - 2 : 0; i < g; ++i) drain_bar(bar(B_O_FULL + (i & 1)), (i >> 1) & 1, hdr, 267);
+        } else if (warp == 9 && lane == 0) {
             // ---------------------------------------------------------- MMA issue
-            uint32_t gq = 0, nu = 0;
+            uint32_t g = 0, nu = 0;  // tiles, units with tiles
             bool stop = false;
+            // column (from a buffer's first) of the bf16 pairs of rows 16 kk .. + 15: warpgroup
+            // kk / 4 wrote its 64 rows over the first 32 columns of its own half
+            auto pcol = [](int kk) { return 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3); };
+            auto issue_dv = [&](uint32_t t, bool first) -> bool {  // dV += P^T dO of tile t
+                if (!wait_bar(bar(B_P_FULL), t & 1, abort, hdr, 268)) return false;
+                tc_fence_after();
+                const uint32_t gb = sDO + (t & 1) * C::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
+                            C::kIdescAcc, (!first || kk > 0));
+                umma_commit(bar(B_O_EMPTY + (t & 1)));
+                return true;
+            };
+            auto issue_dk = [&](uint32_t t, bool first) -> bool {  // dK += dS^T Q of tile t
+                if (!wait_bar(bar(B_DS_FULL), t & 1, abort, hdr, 269)) return false;
+                tc_fence_after();
+                const uint32_t qb = sQ + (t % 3) * C::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_ts(tmem + kColDK, tmem + kColDPT + pcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
+                            C::kIdescAcc, (!first || kk > 0));
+                umma_commit(bar(B_Q_EMPTY + t % 3));
+                return true;
+            };
+            // D[col] = A[sA] B[sB]^T over d
+            auto issue_ss = [&](uint32_t col, uint32_t sa, uint32_t sb) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
+                    umma_ss(tmem + col, sdesc_sw128(sa + off, 16, 1024), sdesc_sw128(sb + off, 16, 1024), C::kIdescSS, kk > 0);
+                }
+            };
             for (int it = 0; !stop; ++it) {
                 const int slot = it & 1;
-                if (!wait_bar(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 264)) break;
+                if (!wait_bar(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 270)) break;
                 const int u = sh.item[slot];
                 mbar_arrive(bar(B_ITEM_EMPTY + slot));
                 if (u < 0) break;
                 Unit x;
                 decode(a, p, u, x);
                 if (x.i0 >= x.i1) continue;
-                if (!wait_bar(bar(B_KV_FULL), nu & 1, abort, hdr, 265)) break;
-                ++nu;
-                tc_fence_after();
-                for (int i = x.i0; i < x.i1; ++i, ++gq) {
-                    const uint32_t st = gq & 1;
-                    if (!wait_bar(bar(B_QT_FULL + st), (gq >> 1) & 1, abort, hdr, 266)) { stop = true; break; }
+                if (!wait_bar(bar(B_KV_FULL), nu & 1, abort, hdr, 271)) break;
+                for (int i = x.i0; i < x.i1; ++i, ++g) {
+                    if (i == x.i0 + 1 && nu > 0 && !wait_bar(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 272)) { stop = true; break; }
+                    if (i > x.i0 && !issue_dv(g - 1, i - 1 == x.i0)) { stop = true; break; }
+                    if (!wait_bar(bar(B_Q_FULL + g % 3), (g / 3) & 1, abort, hdr, 273)) { stop = true; break; }
                     tc_fence_after();
-                    const uint32_t qb = sQ + st * C::kTileBytes, gb = sDO + st * C::kTileBytes;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
-                        umma_ss(tmem + kColST, sdesc_sw128(sK + off, 16, 1024), sdesc_sw128(qb + off, 16, 1024),
-                                C::kIdescSS, kk > 0);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
-                        umma_ss(tmem + kColDPT, sdesc_sw128(sV + off, 16, 1024), sdesc_sw128(gb + off, 16, 1024),
-                                C::kIdescSS, kk > 0);
-                    }
-                    umma_commit(bar(B_ST_FULL));
-                    if (i + 1 == x.i1) umma_commit(bar(B_KV_EMPTY));
-                    if (!wait_bar(bar(B_P_FULL), gq & 1, abort, hdr, 267)) { stop = true; break; }
+                    issue_ss(kColST, sK, sQ + (g % 3) * C::kTileBytes);
+                    umma_commit(bar(B_S_FULL));
+                    if (i > x.i0 && !issue_dk(g - 1, i - 1 == x.i0)) { stop = true; break; }
+                    if (!wait_bar(bar(B_O_FULL + (g & 1)), (g >> 1) & 1, abort, hdr, 274)) { stop = true; break; }
                     tc_fence_after();
-                    // rows 16 kk .. + 15 of P^T / dS^T: warpgroup kk / 4 wrote its 64 rows over the
-                    // first 32 columns of its own half
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t ac = 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3);
-                        umma_ts(tmem + kColDV, tmem + kColST + ac, sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
-                                C::kIdescAcc, (i > x.i0 || kk > 0));
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t ac = 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3);
-                        umma_ts(tmem + kColDK, tmem + kColDPT + ac, sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
-                                C::kIdescAcc, (i > x.i0 || kk > 0));
-                    }
-                    umma_commit(bar(B_QT_EMPTY + st));
+                    issue_ss(kColDPT, sV, sDO + (g & 1) * C::kTileBytes);
+                    umma_commit(bar(B_DP_FULL));
                 }
                 if (stop) break;
+                umma_commit(bar(B_KV_EMPTY));
+                const bool one = x.i1 - x.i0 == 1;
+                if (one && nu > 0 && !wait_bar(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 275)) break;
+                if (!issue_dv(g - 1, one) || !issue_dk(g - 1, one)) break;
                 umma_commit(bar(B_ACC_DONE));
+                ++nu;
             }
             umma_commit(bar(B_MMA_DONE));
-            drain_bar(bar(B_MMA_DONE), 0, hdr, 268);
+            drain_bar(bar(B_MMA_DONE), 0, hdr, 276);
         }
         __syncwarp();
-    } else if (warp >= 8) {
-        regs_dec<kRegsGather>();
-        // -------------------------------------------------------------- row tiles (warps 8-11)
-        const int r = tid - 256, wr = (warp - 8) * 32;
-        constexpr int CH = D / 8;  // 16-byte pieces a row
-        uint32_t gq = 0;
-        for (int it = 0;; ++it) {
-            const int slot = it & 1;
-            if (!wait_bar_warp(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 271)) break;
-            const int u = sh.item[slot];
-            mbar_arrive(bar(B_ITEM_EMPTY + slot));
-            if (u < 0) break;
-            Unit x;
-            decode(a, p, u, x);
-            bool stop = false;
-            for (int i = x.i0; i < x.i1; ++i, ++gq) {
-                int hq, t0, n;
-                row_tile(a, x, i, hq, t0, n);
-                const uint32_t st = gq & 1;
-                if (!wait_bar_warp(bar(B_QT_EMPTY + st), ((gq >> 1) & 1) ^ 1, abort, hdr, 272)) { stop = true; break; }
-                const size_t row0 = (size_t(x.b) * a.Hq + hq) * size_t(a.Lq) + t0;
-                float l2 = INFINITY, dd = 0.f;  // +inf: every p of the row is zero
-                if (r < n) {
-                    const float v = __ldg(lse + row0 + r);
-                    if (v > -INFINITY || v != v) l2 = v * kLog2e;
-                    dd = __ldg(Dsum + row0 + r);
-                }
-                stat[(st * 2 + 0) * 128 + r] = l2;
-                stat[(st * 2 + 1) * 128 + r] = dd;
-#pragma unroll
-                for (int i2 = 0; i2 < CH; ++i2) {
-                    const int idx = i2 * 32 + lane;
-                    const int rr = wr + idx / CH, ch = idx % CH;
-                    const uint32_t off = (ch >> 3) * C::kSlabBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
-                    const size_t src = (row0 + (rr < n ? rr : 0)) * D + ch * 8;
-                    cp_async16(sQ + st * C::kTileBytes + off, Q + src, rr < n ? 16 : 0);
-                    cp_async16(sDO + st * C::kTileBytes + off, dO + src, rr < n ? 16 : 0);
-                }
-                cp_async_commit();
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
-                mbar_arrive(bar(B_QT_FULL + st));
-            }
-            if (stop) break;
-        }
     } else {
         regs_inc<kRegsCompute>();
         // -------------------------------------------------------------- compute (warps 0-7)
-        const int wg = warp >> 2, row = tid & 127;  // rows [64 wg, + 64) of the tile; key of the tile
+        const int wg = warp >> 2, row = tid & 127;  // rows [64 wg, + 64) of the tiles; key of the unit
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t s_addr = lane_addr + kColST + 64 * wg, g_addr = lane_addr + kColDPT + 64 * wg;
         const float sl2 = a.scale * kLog2e;
-        uint32_t gq = 0, nu = 0;
+        uint32_t g = 0, nu = 0, nt = 0;
         for (int it = 0;; ++it) {
             const int slot = it & 1;
-            if (!wait_bar_warp(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 273)) break;
+            if (!wait_bar_warp(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 281)) break;
             const int u = sh.item[slot];
             mbar_arrive(bar(B_ITEM_EMPTY + slot));
             if (u < 0) break;
@@ -702,51 +766,91 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.causal) v_lo = max(v_lo, key);
             const int v_hi = key < a.sinks ? (1 << 30) : key + a.left + 1;
             bool stop = false;
-            for (int i = x.i0; i < x.i1; ++i, ++gq) {
+            for (int i = x.i0; i < x.i1; ++i, ++g) {
                 int hq, t0, n;
                 row_tile(a, x, i, hq, t0, n);
-                const uint32_t st = gq & 1;
-                if (!wait_bar_warp(bar(B_QT_FULL + st), (gq >> 1) & 1, abort, hdr, 274)) { stop = true; break; }
-                if (!wait_bar_warp(bar(B_ST_FULL), gq & 1, abort, hdr, 275)) { stop = true; break; }
+                const uint32_t os = g & 1;
+                // dO and the statistics (their own barrier makes the copies visible here), S^T
+                if (!wait_bar_warp(bar(B_O_FULL + os), (g >> 1) & 1, abort, hdr, 282)) { stop = true; break; }
+                if (!wait_bar_warp(bar(B_S_FULL), g & 1, abort, hdr, 283)) { stop = true; break; }
                 tc_fence_after();
-                const float* l2 = stat + (st * 2 + 0) * 128 + 64 * wg;
-                const float* dd = stat + (st * 2 + 1) * 128 + 64 * wg;
-                const uint32_t s_addr = lane_addr + kColST + 64 * wg, g_addr = lane_addr + kColDPT + 64 * wg;
+                const float4* stat = reinterpret_cast<const float4*>(smem_raw + C::oStat + os * C::kStatBytes) + 32 * wg;
+                if (n < kTile) {
+                    // rows past the last: nothing of theirs (whatever was loaded) may reach a
+                    // product. dP^T may still be reading dO: what it makes of these rows is masked.
+                    if (row >= n) {
+                        if ((row >> 6) == wg)
+                            reinterpret_cast<float2*>(smem_raw + C::oStat + os * C::kStatBytes)[row] = make_float2(INFINITY, 0.f);
+                        const uint32_t dst = (wg == 0 ? sQ + (g % 3) * C::kTileBytes : sDO + os * C::kTileBytes) + row * 128;
+#pragma unroll
+                        for (int c = 0; c < C::kSlabs * 8; ++c)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (c >> 3) * C::kSlabBytes + (c & 7) * 16),
+                                         "r"(0u) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(bar(B_TAIL + wg));  // the statistics above are read by the whole warpgroup
+                    if (!wait_bar_warp(bar(B_TAIL + wg), nt & 1, abort, hdr, 284)) { stop = true; break; }
+                    ++nt;
+                }
                 const int p0 = t0 + x.seq.shift + 64 * wg;
-                const int lo = v_lo - p0, hi = v_hi - p0;
-                if (!__all_sync(0xffffffffu, row >= x.nk || (lo <= 0 && hi >= 64))) {
+                const int lo = v_lo - p0, hi = min(v_hi - p0, n - 64 * wg);
+                const bool masked = !__all_sync(0xffffffffu, n == kTile && (row >= x.nk || (lo <= 0 && hi >= 64)));
+                if (masked) {
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w) mask_cols(s_addr + 32 * w, win::bits(lo - 32 * w, hi - 32 * w), kMinusInf);
                     tmem_wait_st();
                 }
+                uint32_t s[64];
+                tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                tmem_wait_ld_regs(s);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t s[32], g[32];
-                    tmem_ld32(s_addr + 32 * c, s);
-                    tmem_ld32(g_addr + 32 * c, g);
-                    tmem_wait_ld_regs(s);
-                    tmem_wait_ld_regs(g);
-                    uint32_t pp[16], pd[16];
+                    uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int q0 = 32 * c + 2 * e;
-                        const float p0f = ex2(fmaf(__uint_as_float(s[2 * e]), sl2, -l2[q0]));
-                        const float p1f = ex2(fmaf(__uint_as_float(s[2 * e + 1]), sl2, -l2[q0 + 1]));
-                        pp[e] = pack_bf16(p0f, p1f);
-                        pd[e] = pack_bf16(p0f * (__uint_as_float(g[2 * e]) - dd[q0]), p1f * (__uint_as_float(g[2 * e + 1]) - dd[q0 + 1]));
+                        const float4 q = stat[16 * c + e];  // two rows' (log-sum-exp, D)
+                        const float p0f = ex2(fmaf(__uint_as_float(s[32 * c + 2 * e]), sl2, -q.x));
+                        const float p1f = ex2(fmaf(__uint_as_float(s[32 * c + 2 * e + 1]), sl2, -q.z));
+                        pk[e] = pack_bf16(p0f, p1f);
+                        s[32 * c + 2 * e] = __float_as_uint(p0f);
+                        s[32 * c + 2 * e + 1] = __float_as_uint(p1f);
                     }
-                    tmem_st16(s_addr + 16 * c, pp);
-                    tmem_st16(g_addr + 16 * c, pd);
+                    tmem_st16(s_addr + 16 * c, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(B_P_FULL));
+                if (!wait_bar_warp(bar(B_DP_FULL), g & 1, abort, hdr, 285)) { stop = true; break; }
+                tc_fence_after();
+                if (n < kTile) {  // dP^T of a row past the last may be NaN
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w) mask_cols(g_addr + 32 * w, win::bits(0, n - 64 * wg - 32 * w), 0u);
+                    tmem_wait_st();
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t d[32], pk[16];
+                    tmem_ld32(g_addr + 32 * c, d);
+                    tmem_wait_ld_regs(d);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float4 q = stat[16 * c + e];
+                        pk[e] = pack_bf16(__uint_as_float(s[32 * c + 2 * e]) * (__uint_as_float(d[2 * e]) - q.y),
+                                          __uint_as_float(s[32 * c + 2 * e + 1]) * (__uint_as_float(d[2 * e + 1]) - q.w));
+                    }
+                    tmem_st16(g_addr + 16 * c, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(B_DS_FULL));
+                mbar_arrive(bar(B_O_EMPTY + os));
             }
             if (stop) break;
             // this warpgroup's half of the columns of dV and dK for its key rows
             const bool some = x.i0 < x.i1;
             if (some) {
-                if (!wait_bar_warp(bar(B_ACC_DONE), nu & 1, abort, hdr, 276)) break;
+                if (!wait_bar_warp(bar(B_ACC_DONE), nu & 1, abort, hdr, 286)) break;
                 ++nu;
                 tc_fence_after();
             }
@@ -787,12 +891,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_before();
+            if (some) mbar_arrive(bar(B_EPI_DONE));
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -846,13 +951,11 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     const int sms = sm_count();
     const int64_t qrows = int64_t(a.B) * a.Hq * a.Lq, krows = int64_t(a.B) * a.Hk * a.Lk;
     int32_t* work = reinterpret_cast<int32_t*>(ws + p.work);
-    float* dsum = reinterpret_cast<float*>(ws + p.dsum);
+    float2* stats = reinterpret_cast<float2*>(ws + p.stats);
     float* parts = reinterpret_cast<float*>(ws + p.part);
-    const auto* q = static_cast<const __nv_bfloat16*>(Q);
-    const auto* g = static_cast<const __nv_bfloat16*>(dO);
-    const int64_t want = (qrows * (D / 8) + 255) / 256, most = int64_t(sms) * 16;
-    window_rowdot_kernel<D><<<int(want < 1 ? 1 : want < most ? want : most), 256, 0, s>>>(
-        a, static_cast<const __nv_bfloat16*>(O), g, dsum, work);
+    const int64_t want = ((qrows + int64_t(a.B) * a.Hq + 128) * (D / 8) + 255) / 256, most = int64_t(sms) * 16;
+    window_stats_kernel<D><<<int(want < most ? want : most), 256, 0, s>>>(
+        a, static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(dO), lse, stats, work);
     CUtensorMap tmQ, tmDO, tmK, tmV;
     if (krows > 0) {
         if (!make_tmap(&tmK, K, D, krows) || !make_tmap(&tmV, V, D, krows)) return cudaErrorInvalidValue;
@@ -865,7 +968,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         if (e != cudaSuccess) return e;
         const int nqt = (a.Lq + kTile - 1) / kTile, n = a.B * a.Hq * nqt;
         dq::window_dq_kernel<D><<<n < sms ? n : sms, dq::kThreads, smem, s>>>(
-            tmQ, tmDO, tmK, tmV, a, n, nqt, lse, dsum, work, hdr, static_cast<__nv_bfloat16*>(dQ));
+            tmQ, tmDO, tmK, tmV, a, n, nqt, stats, work, hdr, static_cast<__nv_bfloat16*>(dQ));
     }
     if (krows > 0) {
         const int smem = dkv::Cfg<D>::kSmem;
@@ -873,8 +976,9 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         if (e != cudaSuccess) return e;
         const int heads = a.B * a.Hk;
         const int n = heads * (p.key_tiles - p.split_tiles + p.split_tiles * p.splits);
+        if (qrows == 0) tmQ = tmDO = tmK;  // no row tile is loaded
         dkv::window_dkv_kernel<D><<<n < sms ? n : sms, dkv::kThreads, smem, s>>>(
-            tmK, tmV, a, p, n, q, g, lse, dsum, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK),
+            tmK, tmV, tmQ, tmDO, a, p, n, stats, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK),
             static_cast<__nv_bfloat16*>(dV));
         if (p.splits > 1) {
             const int64_t blocks = (int64_t(p.split_tiles) * heads * 2 * 128 * (D / 4) + 255) / 256;
@@ -891,8 +995,8 @@ WinBwdPlan plan_window_bwd(const WinArgs& a, int d) {
     WinBwdPlan p;
     auto align = [](size_t x) { return (x + 255) & ~size_t(255); };
     p.work = 0;
-    p.dsum = 256;
-    p.part = p.dsum + align(size_t(a.B) * a.Hq * a.Lq * sizeof(float));
+    p.stats = 256;
+    p.part = p.stats + align((size_t(a.B) * a.Hq * size_t((a.Lq + 1) & ~1) + 128) * 2 * sizeof(float));
     p.key_tiles = (a.Lk + kTile - 1) / kTile;
     const int sink_tiles = (a.sinks + kTile - 1) / kTile;
     p.split_tiles = sink_tiles < p.key_tiles ? sink_tiles : p.key_tiles;

@@ -113,7 +113,7 @@ cudaError_t window_error_word(int32_t** word);
 // Workspace of the backward pass.
 struct WinBwdPlan {
     size_t work = 0;     // int32[64]: work counters of the dQ and the dK / dV kernel
-    size_t dsum = 0;     // fp32 [B Hq Lq]: D = dO . o
+    size_t stats = 0;    // fp32 [B Hq][Lq up to even][2], + 128: log-sum-exp in exp2 units, D = dO . o
     size_t part = 0;     // fp32 [units][2][128][d]: dV, dK parts of the split key tiles
     size_t total = 0;
     int key_tiles = 0;   // of one (b, key head)
