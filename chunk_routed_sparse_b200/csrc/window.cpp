@@ -52,6 +52,8 @@ extern "C" moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, in
     if (B == 0 || Hq == 0 || Lq == 0) return MOC_OK;
     if (!aligned16(Q) || !aligned16(O) || (Lk > 0 && (!aligned16(K) || !aligned16(V))) || !aligned4(lse))
         return MOC_ERR_INVALID_ARG;
+    if (int64_t(a.group) * Lq <= moc::kWinFewRows && int64_t(B) * Hk <= 65535 && Lk > 0)
+        return cuda_status(moc::launch_window_few(a, d, Q, K, V, O, lse, (cudaStream_t)stream));
     return cuda_status(moc::launch_window_fwd(a, d, Q, K, V, O, lse, (cudaStream_t)stream));
 }
 

@@ -81,6 +81,21 @@ CASES = [  # B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len
     (1, 1, 1, 2112, 2112, 64, 256, 256, 64, False, None, None),   # the tiny scene: captions and a frame either side
 ]
 
+FEW = [  # few rows against a cache: one tile of up to 16 rows (query heads of a key head x rows)
+    (1, 1, 1, 1, 1000, 64, -1, 0, 0, True, None, None),
+    (8, 24, 24, 1, 777, 128, 255, 0, 64, True, None, [777, 1, 0, 64, 65, 320, 500, 700]),
+    (2, 16, 1, 1, 3000, 128, -1, 0, 4, True, None, [3000, 2999]),
+    (2, 8, 2, 4, 515, 64, 100, 0, 7, True, None, None),
+    (3, 6, 2, 5, 1025, 128, 300, 40, 9, False, [5, 0, 3], [1025, 600, 2]),
+    (1, 3, 3, 16, 4100, 128, 1000, 0, 200, True, None, None),
+    (1, 2, 2, 17, 4100, 128, 1000, 0, 200, True, None, None),          # one row too many: the many-row kernel
+    (2, 5, 5, 2, 63, 64, 0, 0, 0, True, None, None),
+    (1, 4, 2, 3, 2, 64, -1, -1, 0, True, None, None),                  # more rows than keys
+    (40, 4, 4, 1, 130, 64, 64, 0, 1, True, None, None),
+    (1, 1, 1, 1, 70000, 128, -1, 0, 0, True, None, None),
+]
+CASES += FEW
+
 
 @pytest.mark.parametrize("case", CASES, ids=str)
 def test_forward_matches_the_definition(case):
@@ -112,6 +127,21 @@ def test_garbage_past_the_lengths_is_not_read():
             for t in (q, k, v):
                 t[b, :, int(n[b]):] = bad
         got = moc.window_attention_fwd(q, k, v, 60, 0, 4, True, n, n)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_few_rows_ignore_garbage_past_the_lengths():
+    B, Hq, Hk, L, d = 3, 8, 2, 500, 128
+    Q, K, V = _qkv(B, Hq, Hk, 2, L, d)
+    n = _lens([170, 500, 33])
+    want = moc.window_attention_fwd(Q, K, V, 60, 0, 4, True, None, n)
+    for bad in (math.nan, math.inf):
+        k, v = K.clone(), V.clone()
+        for b in range(B):
+            k[b, :, int(n[b]):] = v[b, :, int(n[b]):] = bad
+            lo = max(4, int(n[b]) - 2 - 60)  # between the first keys and the window of both rows
+            k[b, :, 4:lo] = v[b, :, 4:lo] = bad
+        got = moc.window_attention_fwd(Q, k, v, 60, 0, 4, True, None, n)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
