@@ -14,14 +14,13 @@ current stream of the tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Sequence, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _check, _ptr, _stream, lib
+from . import MocError, _check, lib
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -87,11 +86,23 @@ class Rope:
             pass
 
 
-def _on(device: torch.device):
-    """The device's context, for the launch and its current stream."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+
+
+def _call(where: str, device: torch.device, *args):
+    """Call lib().<where>(*args, stream) on the device and its current stream."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        status = getattr(lib(), where)(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = getattr(lib(), where)(*args, _raw_stream(i))
+    if status != 0:
+        raise MocError(status, where)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(name: str, x: torch.Tensor, like: Optional[torch.Tensor] = None, shape=None):
@@ -133,16 +144,19 @@ def _positions(rope: Optional[Rope], pos: Optional[torch.Tensor], B: int, L: int
     return pos, pos.stride(0) if pos.dim() == 3 else 0, pos.stride(-2) if pos.dim() > 1 else 0
 
 
+_STRIDES = {n: ctypes.c_int64 * (3 * n) for n in (2, 6, 8)}
+
+
 def _strides(*tensors):
     """Batch, head and token strides of every tensor in one host array, and its address."""
     vals = []
     for t in tensors:
         vals += t.stride()[:3] if t is not None else (0, 0, 0)
-    buf = (ctypes.c_int64 * len(vals))(*vals)
+    buf = _STRIDES[len(tensors)](*vals)
     return buf, ctypes.addressof(buf)
 
 
-def _rotary(rope, X, pos, transpose, out, where):
+def _rotary(rope, X, pos, transpose, out):
     _rows("X", X)
     B, H, L, d = X.shape
     if rope is None:
@@ -153,9 +167,8 @@ def _rotary(rope, X, pos, transpose, out, where):
     else:
         _rows("out", out, X, X.shape)
     buf, at = _strides(X, out)
-    with _on(X.device):
-        _check(lib().moc_rotary(rope.handle, _DTYPE[X.dtype], B, H, L, d, _ptr(X), at, _ptr(p), pb, pa, transpose,
-                                _ptr(out), at + 24, _stream()), where)
+    _call("moc_rotary", X.device, rope.handle, _DTYPE[X.dtype], B, H, L, d, X.data_ptr(), at, _at(p), pb, pa, transpose,
+          out.data_ptr(), at + 24)
     return out
 
 
@@ -163,13 +176,13 @@ def rotary_fwd(rope: Rope, X: torch.Tensor, pos: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = R X (moc_rotary), head-major contiguous unless ``out`` says otherwise;
     ``out`` may be X itself."""
-    return _rotary(rope, X, pos, 0, out, "moc_rotary")
+    return _rotary(rope, X, pos, 0, out)
 
 
 def rotary_bwd(rope: Rope, dY: torch.Tensor, pos: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dX = R^T dY, the gradient of rotary_fwd (moc_rotary, transposed)."""
-    return _rotary(rope, dY, pos, 1, out, "moc_rotary")
+    return _rotary(rope, dY, pos, 1, out)
 
 
 def _dense(g: torch.Tensor) -> torch.Tensor:
@@ -257,11 +270,9 @@ def qk_norm_rope_fwd(Q, K, V=None, wq=None, wk=None, rope: Optional[Rope] = None
         if V is not None:
             _rows("out V", Vo, Q, V.shape)
     buf, at = _strides(Q, K, V, Qo, Ko, Vo)
-    with _on(Q.device):
-        _check(lib().moc_qk_norm_rope(rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
-                                      _ptr(Q), at, _ptr(K), at + 24, _ptr(V), at + 48, _ptr(wq), _ptr(wk), code,
-                                      float(eps), _ptr(p), pb, pa, _ptr(Qo), at + 72, _ptr(Ko), at + 96, _ptr(Vo),
-                                      at + 120, _stream()), "moc_qk_norm_rope")
+    _call("moc_qk_norm_rope", Q.device, rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
+          Q.data_ptr(), at, K.data_ptr(), at + 24, _at(V), at + 48, _at(wq), _at(wk), code, eps, _at(p), pb, pa,
+          Qo.data_ptr(), at + 72, Ko.data_ptr(), at + 96, _at(Vo), at + 120)
     return Qo, Ko, Vo
 
 
@@ -294,20 +305,20 @@ def qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQo, dKo, dVo=None, out=None,
     dwq = torch.empty_like(wq) if want_dw and wq is not None else None
     dwk = torch.empty_like(wk) if want_dw and wk is not None else None
     buf, at = _strides(Q, K, dQo, dKo, dVo, dQ, dK, dV)
-    with _on(Q.device):
-        ws = None
-        if dwq is not None or dwk is not None:
-            n = int(lib().moc_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, d))
-            if n == 0:
-                raise ValueError("invalid problem for the workspace size query")
-            ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
-        _check(lib().moc_qk_norm_rope_bwd(rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
-                                          _ptr(Q), at, _ptr(K), at + 24, _ptr(wq), _ptr(wk), code, float(eps),
-                                          _ptr(p), pb, pa, _ptr(dQo), at + 48, _ptr(dKo), at + 72, _ptr(dVo), at + 96,
-                                          _ptr(dQ), at + 120, _ptr(dK), at + 144, _ptr(dV), at + 168, _ptr(dwq),
-                                          _ptr(dwk), _ptr(ws), ws.numel() if ws is not None else 0, _stream()),
-               "moc_qk_norm_rope_bwd")
+    ws = _bwd_workspace(Q.device, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None
+    _call("moc_qk_norm_rope_bwd", Q.device, rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
+          Q.data_ptr(), at, K.data_ptr(), at + 24, _at(wq), _at(wk), code, eps, _at(p), pb, pa, dQo.data_ptr(), at + 48,
+          dKo.data_ptr(), at + 72, _at(dVo), at + 96, dQ.data_ptr(), at + 120, dK.data_ptr(), at + 144, _at(dV),
+          at + 168, _at(dwq), _at(dwk), _at(ws), ws.numel() if ws is not None else 0)
     return dQ, dK, dV, dwq, dwk
+
+
+def _bwd_workspace(device, B, Hq, Hk, L, d):
+    with torch.cuda.device(device):
+        n = int(lib().moc_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, d))
+    if n == 0:
+        raise ValueError("invalid problem for the workspace size query")
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _split(x: torch.Tensor, Hq: int, Hk: int):
@@ -324,8 +335,27 @@ def _packed(qkv, Hq, Hk):
 
 def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=None, eps: float = 1e-6):
     """qk_norm_rope_fwd on the packed projection [B, L, Hq + 2 Hk, d]."""
-    Q, K, V = _packed(qkv, Hq, Hk)
-    return qk_norm_rope_fwd(Q, K, V, wq, wk, rope, pos, eps)
+    _rows("qkv", qkv)
+    B, L, heads, d = qkv.shape
+    if Hq < 1 or Hk < 1 or heads != Hq + 2 * Hk:
+        raise ValueError(f"qkv: expected [B, L, Hq + 2 Hk, d] with Hq = {Hq}, Hk = {Hk}")
+    code = _weights(wq, wk, qkv, d)
+    p, pb, pa = _positions(rope, pos, B, L, d, qkv.device)
+    dt, dev = qkv.dtype, qkv.device
+    Q = torch.empty((B, Hq, L, d), dtype=dt, device=dev)
+    K = torch.empty((B, Hk, L, d), dtype=dt, device=dev)
+    V = torch.empty((B, Hk, L, d), dtype=dt, device=dev)
+    if not qkv.numel():
+        return Q, K, V
+    sb, sl, sh, _ = qkv.stride()
+    oq, ok = (Hq * L * d, L * d, d), (Hk * L * d, L * d, d)
+    buf = _STRIDES[6](sb, sh, sl, sb, sh, sl, sb, sh, sl, *oq, *ok, *ok)
+    at = ctypes.addressof(buf)
+    x, step = qkv.data_ptr(), sh * qkv.element_size()
+    _call("moc_qk_norm_rope", dev, rope.handle if rope is not None else None, _DTYPE[dt], B, Hq, Hk, L, d, x, at,
+          x + Hq * step, at + 24, x + (Hq + Hk) * step, at + 48, _at(wq), _at(wk), code, eps, _at(p), pb, pa,
+          Q.data_ptr(), at + 72, K.data_ptr(), at + 96, V.data_ptr(), at + 120)
+    return Q, K, V
 
 
 def qkv_norm_rope_bwd(qkv, Hq: int, Hk: int, wq, wk, rope, pos, eps, dQ, dK, dV, want_dw: bool = True):

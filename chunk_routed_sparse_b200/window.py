@@ -20,8 +20,8 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _check, _ptr, _stream, lib
-from .rows import _on
+from . import _check, lib
+from .rows import _at, _call
 
 
 def _tensor(name, x, shape, device, dtype=torch.bfloat16):
@@ -68,10 +68,8 @@ def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 
             lse.fill_(-math.inf)
     else:
         _tensor("lse", lse, (B, Hq, Lq), Q.device, torch.float32)
-    with _on(Q.device):
-        _check(lib().moc_window_attention(B, Hq, Hk, Lq, Lk, d, _ptr(Q), _ptr(K), _ptr(V), left, right, sinks,
-                                          1 if causal else 0, _ptr(q_len), _ptr(kv_len), float(scale), _ptr(O),
-                                          _ptr(lse), _stream()), "moc_window_attention")
+    _call("moc_window_attention", Q.device, B, Hq, Hk, Lq, Lk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(), left, right,
+          sinks, 1 if causal else 0, _at(q_len), _at(kv_len), scale, O.data_ptr(), lse.data_ptr())
     return O, lse
 
 
@@ -93,19 +91,18 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
     dQ = (torch.empty_like(Q) if q_len is None else torch.zeros_like(Q)) if dQ is None else dQ
     dK = (torch.empty_like(K) if kv_len is None else torch.zeros_like(K)) if dK is None else dK
     dV = (torch.empty_like(K) if kv_len is None else torch.zeros_like(K)) if dV is None else dV
-    with _on(Q.device):
-        if ws is None:
+    if ws is None:
+        with torch.cuda.device(Q.device):
             n = int(lib().moc_window_attention_bwd_workspace_bytes(B, Hq, Hk, Lq, Lk, d, left, right, sinks,
                                                                    1 if causal else 0))
-            if n == 0:
-                raise ValueError("invalid problem for the backward workspace size query")
-            ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
-        elif ws.device != Q.device or not ws.is_contiguous():
-            raise ValueError(f"ws: expected a contiguous tensor on {Q.device}")
-        _check(lib().moc_window_attention_bwd(B, Hq, Hk, Lq, Lk, d, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
-                                              _ptr(dO), left, right, sinks, 1 if causal else 0, _ptr(q_len),
-                                              _ptr(kv_len), float(scale), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws),
-                                              ws.numel() * ws.element_size(), _stream()), "moc_window_attention_bwd")
+        if n == 0:
+            raise ValueError("invalid problem for the backward workspace size query")
+        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+    elif ws.device != Q.device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {Q.device}")
+    _call("moc_window_attention_bwd", Q.device, B, Hq, Hk, Lq, Lk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+          O.data_ptr(), lse.data_ptr(), dO.data_ptr(), left, right, sinks, 1 if causal else 0, _at(q_len), _at(kv_len),
+          scale, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dQ, dK, dV
 
 
@@ -142,5 +139,6 @@ def check_window_error() -> int:
     """Read and clear the current device's error word of the window calls
     (synchronises); raises MocError on a recorded device error."""
     det = ctypes.c_int32()
-    _check(lib().moc_window_device_error(ctypes.byref(det), _stream()), "window device error word")
+    stream = torch.cuda.current_stream().cuda_stream
+    _check(lib().moc_window_device_error(ctypes.byref(det), stream), "window device error word")
     return det.value
