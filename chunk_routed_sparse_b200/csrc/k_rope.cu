@@ -12,8 +12,11 @@
 // head-major ones costs nothing more. A group of d / 8 lanes holds one row, eight
 // elements a lane, in registers; a group keeps one token and walks the heads, so
 // that the token's cosines and sines are formed once for all of them. Four rows
-// are requested before the first is used. 256 threads: 16 (d = 128) or 32 (d = 64)
-// tokens a CTA, whose outputs are one 4 KB run per head.
+// are requested before the first is used. Many small CTAs (128 threads: 8 or 16
+// tokens, eight an SM) hide the memory's latency: 256 threads cost 9 % on the
+// eight-shot projection (1.15 against 1.05 ms), requesting the next rows ahead costs
+// more registers than it gives, and addressing every row anew costs 8 % (a third of
+// the issue slots are in use). Outputs are streaming stores: nothing here reads them.
 //
 // Angles: the position times a 64-bit fraction of a turn, modulo 2^64, is exact
 // for every 32-bit position (an fp32 product loses 0.01 rad at position 180,000);
@@ -22,11 +25,12 @@
 
 #include "common.cuh"
 #include "rope.cuh"
+#include "sm100.cuh"
 
 namespace moc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kRows = 4;  // rows of one lane group in flight
 
 // ---- eight elements of a row -------------------------------------------------
@@ -64,8 +68,8 @@ __device__ __forceinline__ void store_raw(T* p, const Raw<T>& r) {
     if constexpr (AL) {
 #pragma unroll
         for (int i = 0; i < Raw<T>::kWords; i += 4)
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) =
-                make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+            __stcs(reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i),
+                   make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]));
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) reinterpret_cast<uint32_t*>(p)[i] = r.w[i];
@@ -124,12 +128,19 @@ __device__ __forceinline__ float one(const T* p, int i) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load_w(const void* w, int w_fp32, int e0, float (&v)[8]) {
+__device__ __forceinline__ float weight(const void* w, int w_fp32, int e) {
+    return w == nullptr ? 1.f : w_fp32 ? static_cast<const float*>(w)[e] : one(static_cast<const T*>(w), e);
+}
+
+// sum of eight products, on packed fp32 pairs
+__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
+    uint64_t s = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = w == nullptr ? 1.f
-               : w_fp32    ? static_cast<const float*>(w)[e0 + i]
-                           : one(static_cast<const T*>(w), e0 + i);
+    for (int j = 0; j < 4; ++j)
+        s = sm100::f2_fma(sm100::f2_pack(x[2 * j], x[2 * j + 1]), sm100::f2_pack(y[2 * j], y[2 * j + 1]), s);
+    float lo, hi;
+    sm100::f2_unpack(s, lo, hi);
+    return lo + hi;
 }
 
 // sum over the LPR lanes of a row
@@ -262,7 +273,10 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
         const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0;
         T* y = static_cast<T*>(sec.y) + b * sec.ys[0] + l * sec.ys[2] + e0;
         float w[8];
-        if (sec.mode == ROW_NORM) load_w<T>(sec.w, a.w_fp32, e0, w);
+        if (sec.mode == ROW_NORM) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = weight<T>(sec.w, a.w_fp32, e0 + j);
+        }
 #pragma unroll 1
         for (int h = lo; h < hi; h += kRows) {
             Raw<T> raw[kRows];
@@ -276,10 +290,7 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
                     float v[8];
                     unpack<T>(raw[u], v);
                     if (sec.mode == ROW_NORM) {
-                        float ss = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-                        const float rs = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+                        const float rs = rsqrtf(row_sum<LPR>(dot8(v, v)) * (1.f / D) + a.eps);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * w[j];
                     }
@@ -293,36 +304,42 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
 }
 
 // ---- backward of norm + rotation ---------------------------------------------
-// A persistent CTA strides over token tiles and keeps its part of dw in
-// registers; the parts of a CTA are added through shared memory in thread order
-// and those of all CTAs by rows_dw_kernel in CTA order: no atomics.
+// A persistent CTA strides over token tiles, one tensor after the other (one
+// weight's partial gradient in registers at a time); the parts of a CTA are added
+// through shared memory in thread order and those of all CTAs by rows_dw_kernel in
+// CTA order: no atomics. Four rows of each tensor in flight a lane group, four CTAs
+// an SM: 160 us on the single-shot step (126 us of bytes at the measured copy rate)
+// against 165 us with two rows and five CTAs.
 template <typename T, int D, bool HALF, bool AL>
-__global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int LPR = D / 8, TPC = kThreads / LPR, ROWS = 2;
+__global__ void __launch_bounds__(kThreads, 4) rows_bwd_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int LPR = D / 8, TPC = kThreads / LPR, ROWS = sizeof(T) == 4 ? 2 : 4;
     __shared__ uint64_t turn[kMaxRopePairs];
     __shared__ uint8_t axis[kMaxRopePairs];
+    __shared__ __align__(16) float ws[D];
     __shared__ float red[TPC][D];
     tab_to_smem(a, turn, axis);
     const int r = threadIdx.x % LPR, e0 = 8 * r;
-    float dw[2][8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
     const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
-    for (int64_t t0 = int64_t(blockIdx.x) * TPC; t0 < a.tokens; t0 += int64_t(gridDim.x) * TPC) {
-        const int64_t tok = t0 + threadIdx.x / LPR;
-        const bool live = tok < a.tokens;
-        const int t = live ? int(tok) : a.tokens - 1;
-        const int b = t / a.L, l = t - b * a.L;
-        Trig<HALF> tr;
-        trig<HALF>(a, turn, axis, b, l, e0, tr);
-        int base = 0;
+    int base = 0;
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {
+        const RowSec& sec = a.sec[k];
+        const int lo = max(h_lo - base, 0), hi = min(h_hi - base, sec.H);
+        base += sec.H;
+        if (k < 2) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < D; i += kThreads) ws[i] = weight<T>(sec.w, a.w_fp32, i);
+            __syncthreads();
+        }
+        float dw[8];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const RowSec& sec = a.sec[k];
-            const int lo = max(h_lo - base, 0), hi = min(h_hi - base, sec.H);
-            base += sec.H;
-            if (lo >= hi) continue;
-            const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0;
+        for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+#pragma unroll 1
+        for (int64_t t0 = int64_t(blockIdx.x) * TPC; lo < hi && t0 < a.tokens; t0 += int64_t(gridDim.x) * TPC) {
+            const int64_t tok = t0 + threadIdx.x / LPR;
+            const bool live = tok < a.tokens;
+            const int t = live ? int(tok) : a.tokens - 1;
+            const int b = t / a.L, l = t - b * a.L;
             const T* g = static_cast<const T*>(sec.g) + b * sec.gs[0] + l * sec.gs[2] + e0;
             T* y = static_cast<T*>(sec.y) + b * sec.ys[0] + l * sec.ys[2] + e0;
             if (k == 2) {  // values: the gradient only changes its layout
@@ -338,8 +355,9 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constan
                 }
                 continue;
             }
-            float w[8];
-            load_w<T>(sec.w, a.w_fp32, e0, w);
+            const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0;
+            Trig<HALF> tr;
+            trig<HALF>(a, turn, axis, b, l, e0, tr);
 #pragma unroll 1
             for (int h = lo; h < hi; h += ROWS) {
                 Raw<T> rx[ROWS], rg[ROWS];
@@ -353,25 +371,21 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constan
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u) {
                     if (h + u >= hi) break;
-                    float v[8], q[8];
+                    float v[8], q[8], w[8];
                     unpack<T>(rx[u], v);
                     unpack<T>(rg[u], q);
                     rotate<LPR, HALF>(q, tr, a.rope.pairs, r, e0);
-                    float ss = 0.f, sg = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ss = fmaf(v[j], v[j], ss);
-                        sg = fmaf(q[j] * w[j], v[j], sg);
-                    }
-                    ss = row_sum<LPR>(ss);
-                    sg = row_sum<LPR>(sg);
+                    const float4 wa = *reinterpret_cast<const float4*>(&ws[e0]), wb = *reinterpret_cast<const float4*>(&ws[e0 + 4]);
+                    w[0] = wa.x * q[0], w[1] = wa.y * q[1], w[2] = wa.z * q[2], w[3] = wa.w * q[3];  // g w
+                    w[4] = wb.x * q[4], w[5] = wb.y * q[5], w[6] = wb.z * q[6], w[7] = wb.w * q[7];
+                    const float ss = row_sum<LPR>(dot8(v, v)), sg = row_sum<LPR>(dot8(w, v));
                     const float rs = rsqrtf(ss * (1.f / D) + a.eps);
                     const float m = sg * rs * (1.f / D);  // mean(g w xhat)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float xh = v[j] * rs;
-                        if (live) dw[k][j] = fmaf(q[j], xh, dw[k][j]);
-                        v[j] = rs * (q[j] * w[j] - xh * m);
+                        if (live) dw[j] = fmaf(q[j], xh, dw[j]);
+                        v[j] = rs * (w[j] - xh * m);
                     }
                     Raw<T> ry;
                     pack<T>(v, ry);
@@ -379,15 +393,12 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const __grid_constan
                 }
             }
         }
-    }
-    if (a.part == nullptr) return;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
+        if (k == 2 || a.part == nullptr) continue;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) red[threadIdx.x / LPR][e0 + j] = dw[k][j];
+        for (int j = 0; j < 8; ++j) red[threadIdx.x / LPR][e0 + j] = dw[j];
         __syncthreads();
-        if (threadIdx.x < D) {
+        if (threadIdx.x < D) {  // kThreads >= D
             float s = 0.f;
             for (int i = 0; i < TPC; ++i) s += red[i][threadIdx.x];
             a.part[((size_t(blockIdx.y) * gridDim.x + blockIdx.x) * 2 + k) * D + threadIdx.x] = s;
@@ -444,10 +455,10 @@ int sm_count() {
 }  // namespace
 
 // Token tiles on x (at most `most`, CTAs stride over the rest), heads split on y
-// only while that gives fewer than four CTAs an SM: a split forms the token's
+// only while that gives fewer than eight CTAs an SM: a split forms the token's
 // cosines again.
 static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t most, int* heads_per_cta) {
-    const int64_t tpc = kThreads * 8 / d, want = 4 * int64_t(sm_count());
+    const int64_t tpc = kThreads * 8 / d, want = 8 * int64_t(sm_count());
     int64_t tiles = (tokens + tpc - 1) / tpc;
     int64_t split = tiles >= want ? 1 : (want + tiles - 1) / tiles;
     if (split > heads) split = heads;
@@ -457,7 +468,7 @@ static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t most, int* heads
 }
 
 static dim3 rows_bwd_grid(int d, int64_t tokens, int heads, int* heads_per_cta) {
-    return rows_grid(d, tokens, heads, 4 * int64_t(sm_count()), heads_per_cta);
+    return rows_grid(d, tokens, heads, 4 * int64_t(sm_count()), heads_per_cta);  // four CTAs an SM are resident
 }
 
 cudaError_t launch_rows_fwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {

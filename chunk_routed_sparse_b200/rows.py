@@ -89,6 +89,14 @@ class Rope:
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
 
 
+def _on(device: torch.device, fn, *args):
+    """fn(*args) with the device current."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _call(where: str, device: torch.device, *args):
     """Call lib().<where>(*args, stream) on the device and its current stream."""
     i = device.index
@@ -314,31 +322,24 @@ def qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQo, dKo, dVo=None, out=None,
 
 
 def _bwd_workspace(device, B, Hq, Hk, L, d):
-    with torch.cuda.device(device):
-        n = int(lib().moc_qk_norm_rope_bwd_workspace_bytes(B, Hq, Hk, L, d))
+    n = _on(device, lib().moc_qk_norm_rope_bwd_workspace_bytes, B, Hq, Hk, L, d)
     if n == 0:
         raise ValueError("invalid problem for the workspace size query")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _split(x: torch.Tensor, Hq: int, Hk: int):
-    """Head-major views of a packed [B, L, Hq + 2 Hk, d] projection."""
-    t = x.transpose(1, 2)
-    return t[:, :Hq], t[:, Hq:Hq + Hk], t[:, Hq + Hk:]
-
-
-def _packed(qkv, Hq, Hk):
-    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 4 or Hq < 1 or Hk < 1 or qkv.shape[2] != Hq + 2 * Hk:
-        raise ValueError(f"qkv: expected [B, L, Hq + 2 Hk, d] with Hq = {Hq}, Hk = {Hk}")
-    return _split(qkv, Hq, Hk)
-
-
-def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=None, eps: float = 1e-6):
-    """qk_norm_rope_fwd on the packed projection [B, L, Hq + 2 Hk, d]."""
+def _packed(qkv, Hq: int, Hk: int):
+    """(B, L, d) of a packed [B, L, Hq + 2 Hk, d] projection."""
     _rows("qkv", qkv)
     B, L, heads, d = qkv.shape
     if Hq < 1 or Hk < 1 or heads != Hq + 2 * Hk:
         raise ValueError(f"qkv: expected [B, L, Hq + 2 Hk, d] with Hq = {Hq}, Hk = {Hk}")
+    return B, L, d
+
+
+def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=None, eps: float = 1e-6):
+    """qk_norm_rope_fwd on the packed projection [B, L, Hq + 2 Hk, d]."""
+    B, L, d = _packed(qkv, Hq, Hk)
     code = _weights(wq, wk, qkv, d)
     p, pb, pa = _positions(rope, pos, B, L, d, qkv.device)
     dt, dev = qkv.dtype, qkv.device
@@ -348,8 +349,7 @@ def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=No
     if not qkv.numel():
         return Q, K, V
     sb, sl, sh, _ = qkv.stride()
-    oq, ok = (Hq * L * d, L * d, d), (Hk * L * d, L * d, d)
-    buf = _STRIDES[6](sb, sh, sl, sb, sh, sl, sb, sh, sl, *oq, *ok, *ok)
+    buf = _STRIDES[6](sb, sh, sl, sb, sh, sl, sb, sh, sl, Hq * L * d, L * d, d, Hk * L * d, L * d, d, Hk * L * d, L * d, d)
     at = ctypes.addressof(buf)
     x, step = qkv.data_ptr(), sh * qkv.element_size()
     _call("moc_qk_norm_rope", dev, rope.handle if rope is not None else None, _DTYPE[dt], B, Hq, Hk, L, d, x, at,
@@ -360,9 +360,29 @@ def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=No
 
 def qkv_norm_rope_bwd(qkv, Hq: int, Hk: int, wq, wk, rope, pos, eps, dQ, dK, dV, want_dw: bool = True):
     """Gradient of qkv_norm_rope_fwd: (dqkv packed and contiguous, dwq, dwk)."""
-    Q, K, _ = _packed(qkv, Hq, Hk)
-    dqkv = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
-    _, _, _, dwq, dwk = qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQ, dK, dV, _split(dqkv, Hq, Hk), want_dw)
+    B, L, d = _packed(qkv, Hq, Hk)
+    _rows("dQ", dQ, qkv, (B, Hq, L, d))
+    _rows("dK", dK, qkv, (B, Hk, L, d))
+    _rows("dV", dV, qkv, (B, Hk, L, d))
+    code = _weights(wq, wk, qkv, d)
+    p, pb, pa = _positions(rope, pos, B, L, d, qkv.device)
+    dev = qkv.device
+    dqkv = torch.empty(qkv.shape, dtype=qkv.dtype, device=dev)
+    dwq = torch.empty_like(wq) if want_dw and wq is not None else None
+    dwk = torch.empty_like(wk) if want_dw and wk is not None else None
+    ws = _bwd_workspace(dev, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None
+    sb, sl, sh, _ = qkv.stride()
+    heads = Hq + 2 * Hk
+    ob, ol = L * heads * d, heads * d
+    buf = _STRIDES[8](sb, sh, sl, sb, sh, sl, *dQ.stride()[:3], *dK.stride()[:3], *dV.stride()[:3], ob, d, ol, ob, d, ol,
+                      ob, d, ol)
+    at, x, y, eb = ctypes.addressof(buf), qkv.data_ptr(), dqkv.data_ptr(), qkv.element_size()
+    if not qkv.numel():  # no rows: addresses mean nothing, the weights' gradients are zero
+        return dqkv, *(None if w is None else w.zero_() for w in (dwq, dwk))
+    _call("moc_qk_norm_rope_bwd", dev, rope.handle if rope is not None else None, _DTYPE[qkv.dtype], B, Hq, Hk, L, d,
+          x, at, x + Hq * sh * eb, at + 24, _at(wq), _at(wk), code, eps, _at(p), pb, pa, dQ.data_ptr(), at + 48,
+          dK.data_ptr(), at + 72, dV.data_ptr(), at + 96, y, at + 120, y + Hq * d * eb, at + 144,
+          y + (Hq + Hk) * d * eb, at + 168, _at(dwq), _at(dwk), _at(ws), ws.numel() if ws is not None else 0)
     return dqkv, dwq, dwk
 
 
