@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = &sh.abort;
     int32_t* const hdr = g_window_err;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1) ? 128 : 1);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
     const int n_rounds = (n_items + int(gridDim.x) - 1) / int(gridDim.x);
 
     if (warp >= 8) {
@@ -235,8 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 if (nq[q] > 0) drain_bar(bar(B_Q_FULL + q), (nq[q] - 1) & 1, hdr, 206);
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9) {
             // ---------------------------------------------------------- MMA issue
+            // The whole warp walks the tiles and one elected lane issues, so that addresses
+            // and descriptors stay in uniform registers: issued from a divergent lane, a
+            // product of eight MMAs took 700 cycles to issue, longer than it runs.
+            const bool leader = elect_one();
             uint32_t gt = 0;                 // key tiles
             uint32_t np[2] = {0, 0};         // tiles of A / B (S_FULL, P_FULL, PV_DONE phases)
             uint32_t nq[2] = {0, 0};         // Q tiles
@@ -244,16 +248,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool fresh[2] = {false, false};  // that PV is the item's first
             bool stop = false;
             // O_q += P_q V of the previous key tile
-            auto issue_pv = [&](int q) -> bool {
-                const uint32_t pst = (gt - 1) & 1;
-                if (!wait_bar(bar(B_P_FULL + q), (np[q] - 1) & 1, abort, hdr, 211)) return false;
+            auto issue_pv = [&](const int q) -> bool {
+                if (!wait_bar_warp(bar(B_P_FULL + q), (np[q] - 1) & 1, abort, hdr, 211)) return false;
                 tc_fence_after();
+                const uint32_t vb = sV + ((gt - 1) & 1) * C::kTileBytes;
+                const uint32_t acc = fresh[q] ? 0u : 1u;
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_ts(tmem + col_o(q), tmem + col_s(q) + kk * 8,
-                            sdesc_sw128(sV + pst * C::kTileBytes + kk * 2048, C::kSlabBytes, 1024), C::kIdescPV,
-                            (!fresh[q] || kk > 0));
-                umma_commit(bar(B_PV_DONE + q));
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(tmem + col_o(q), tmem + col_s(q) + kk * 8, sdesc_sw128(vb + kk * 2048, C::kSlabBytes, 1024),
+                                C::kIdescPV, kk > 0 ? 1u : acc);
+                    umma_commit(bar(B_PV_DONE + q));
+                }
+                __syncwarp();
                 pend[q] = fresh[q] = false;
                 return true;
             };
@@ -263,53 +270,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item x;
                 decode(a, nqt, item, x);
                 const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
+                const int tiles = uniform(x.tiles);
                 bool have[2] = {false, false};
-                for (int j = 0; j < x.tiles; ++j) {
+                for (int j = 0; j < tiles; ++j) {
                     int key0, end;
                     win::tile(x.all, j, key0, end);
                     const uint32_t st = gt & 1;
-                    if (gt > 0 && !wait_bar(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 212)) { stop = true; break; }
+                    if (gt > 0 && !wait_bar_warp(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 212)) { stop = true; break; }
                     bool k_ready = false;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         if (pend[q] && !issue_pv(q)) { stop = true; break; }
                         if (!k_ready) {
-                            if (!wait_bar(bar(B_K_FULL + st), (gt >> 1) & 1, abort, hdr, 213)) { stop = true; break; }
+                            if (!wait_bar_warp(bar(B_K_FULL + st), (gt >> 1) & 1, abort, hdr, 213)) { stop = true; break; }
                             k_ready = true;
                         }
-                        if (!qt[q].sees(key0, end)) continue;
+                        if (!uniform(qt[q].sees(key0, end))) continue;
                         if (!have[q]) {
-                            if (!wait_bar(bar(B_Q_FULL + q), nq[q] & 1, abort, hdr, 214)) { stop = true; break; }
+                            if (!wait_bar_warp(bar(B_Q_FULL + q), nq[q] & 1, abort, hdr, 214)) { stop = true; break; }
                             have[q] = fresh[q] = true;
                             ++nq[q];
                         }
                         tc_fence_after();
                         const uint32_t qb = sQ + q * C::kTileBytes, kb = sK + st * C::kTileBytes;
+                        const bool last = uniform(j == qt[q].last);
+                        if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
-                            umma_ss(tmem + col_s(q), sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
-                                    C::kIdescQK, kk > 0);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
+                                umma_ss(tmem + col_s(q), sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
+                                        C::kIdescQK, kk > 0);
+                            }
+                            umma_commit(bar(B_S_FULL + q));
+                            if (last) umma_commit(bar(B_Q_EMPTY + q));  // its Q rows may be replaced
                         }
-                        umma_commit(bar(B_S_FULL + q));
+                        __syncwarp();
                         pend[q] = true;
                         ++np[q];
-                        if (j == qt[q].last) umma_commit(bar(B_Q_EMPTY + q));  // its Q rows may be replaced
                     }
                     if (stop) break;
-                    if (gt > 0) umma_commit(bar(B_V_EMPTY + ((gt - 1) & 1)));
-                    umma_commit(bar(B_K_EMPTY + st));
+                    if (leader) {
+                        if (gt > 0) umma_commit(bar(B_V_EMPTY + ((gt - 1) & 1)));
+                        umma_commit(bar(B_K_EMPTY + st));
+                    }
+                    __syncwarp();
                     ++gt;
                 }
             }
             if (!stop && gt > 0) {
-                if (wait_bar(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 215)) {
+                if (wait_bar_warp(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 215)) {
                     bool ok = !pend[0] || issue_pv(0);
                     if (ok && pend[1]) issue_pv(1);
                 }
             }
-            umma_commit(bar(B_MMA_DONE));  // TMEM is released after every MMA
-            drain_bar(bar(B_MMA_DONE), 0, hdr, 216);
+            if (leader) {
+                umma_commit(bar(B_MMA_DONE));  // TMEM is released after every MMA
+                drain_bar(bar(B_MMA_DONE), 0, hdr, 216);
+            }
         }
         __syncwarp();
     } else {

@@ -210,6 +210,20 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     return uint32_t(r);
 }
 
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+// A value that is the same in every lane of a converged warp, as one that the
+// compiler may keep in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Warpgroup register reallocation: every warp of the warpgroup executes it.
 template <int N>
 __device__ __forceinline__ void regs_inc() {
