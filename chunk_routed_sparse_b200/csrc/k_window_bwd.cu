@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw + C::oBar + 8 * B_COUNT);
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) {
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
 
     if (warp >= 8) {
         regs_dec<kRegsOther>();
@@ -252,77 +252,94 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t g = gk >= 3 ? gk - 3 : 0; g < gk; ++g) drain_bar(bar(B_K_FULL + g % 3), (g / 3) & 1, hdr, 235);
             for (uint32_t g = gv >= 2 ? gv - 2 : 0; g < gv; ++g) drain_bar(bar(B_V_FULL + (g & 1)), (g >> 1) & 1, hdr, 236);
             if (nu > 0) drain_bar(bar(B_QDO_FULL), (nu - 1) & 1, hdr, 237);
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9) {
             // ---------------------------------------------------------- MMA issue
+            // the whole warp walks the tiles, one elected lane issues (uniform descriptors)
+            const bool leader = elect_one();
             uint32_t gk = 0, gv = 0, gt = 0, nu = 0;
             bool stop = false;
             auto issue_s = [&](uint32_t kt, int b) -> bool {  // S(b) = Q K(kt)^T
                 const uint32_t ks = kt % 3;
-                if (!wait_bar(bar(B_K_FULL + ks), (kt / 3) & 1, abort, hdr, 241)) return false;
+                if (!wait_bar_warp(bar(B_K_FULL + ks), (kt / 3) & 1, abort, hdr, 241)) return false;
                 tc_fence_after();
                 const uint32_t kb = sK + ks * C::kTileBytes;
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
-                    umma_ss(tmem + col_s(b), sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
-                            C::kIdescSS, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
+                        umma_ss(tmem + col_s(b), sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024),
+                                C::kIdescSS, kk > 0);
+                    }
+                    umma_commit(bar(B_S_FULL + b));
                 }
-                umma_commit(bar(B_S_FULL + b));
+                __syncwarp();
                 return true;
             };
             auto issue_dp = [&]() -> bool {  // dP = dO V(gv)^T, then V(gv) is free
                 const uint32_t vs = gv & 1;
-                if (!wait_bar(bar(B_V_FULL + vs), (gv >> 1) & 1, abort, hdr, 242)) return false;
+                if (!wait_bar_warp(bar(B_V_FULL + vs), (gv >> 1) & 1, abort, hdr, 242)) return false;
                 tc_fence_after();
                 const uint32_t vb = sV + vs * C::kTileBytes;
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
-                    umma_ss(tmem + kColDP, sdesc_sw128(sDO + off, 16, 1024), sdesc_sw128(vb + off, 16, 1024),
-                            C::kIdescSS, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
+                        umma_ss(tmem + kColDP, sdesc_sw128(sDO + off, 16, 1024), sdesc_sw128(vb + off, 16, 1024),
+                                C::kIdescSS, kk > 0);
+                    }
+                    umma_commit(bar(B_DP_FULL));
+                    umma_commit(bar(B_V_EMPTY + vs));
                 }
-                umma_commit(bar(B_DP_FULL));
-                umma_commit(bar(B_V_EMPTY + vs));
+                __syncwarp();
                 ++gv;
                 return true;
             };
             for (int it = 0; !stop; ++it) {
                 const int slot = it & 1;
-                if (!wait_bar(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 243)) break;
-                const int u = sh.item[slot];
-                mbar_arrive(bar(B_ITEM_EMPTY + slot));
+                if (!wait_bar_warp(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 243)) break;
+                const int u = uniform(sh.item[slot]);
+                if (leader) mbar_arrive(bar(B_ITEM_EMPTY + slot));
+                __syncwarp();
                 if (u < 0) break;
                 Unit x;
                 decode(a, nqt, u, x);
-                const int T = x.probe + x.tiles;
+                const int probe = uniform(x.probe), T = uniform(x.probe + x.tiles);
                 if (T == 0) continue;
-                if (!wait_bar(bar(B_QDO_FULL), nu & 1, abort, hdr, 244)) break;
+                if (!wait_bar_warp(bar(B_QDO_FULL), nu & 1, abort, hdr, 244)) break;
                 ++nu;
                 tc_fence_after();
                 if (!issue_s(gk, 0) || !issue_dp() || (T > 1 && !issue_s(gk + 1, 1))) break;
-                if (T == 1) umma_commit(bar(B_QDO_EMPTY));
+                if (T == 1 && leader) umma_commit(bar(B_QDO_EMPTY));
+                __syncwarp();
                 for (int j = 0; j < T; ++j) {
-                    if (!wait_bar(bar(B_DS_FULL), gt & 1, abort, hdr, 245)) { stop = true; break; }
+                    if (!wait_bar_warp(bar(B_DS_FULL), gt & 1, abort, hdr, 245)) { stop = true; break; }
                     tc_fence_after();
                     ++gt;
                     if (j + 1 < T && !issue_dp()) { stop = true; break; }
-                    if (T > 1 && j == T - 2) umma_commit(bar(B_QDO_EMPTY));  // the last S was issued before it
+                    if (T > 1 && j == T - 2 && leader) umma_commit(bar(B_QDO_EMPTY));  // the last S was issued before it
                     const uint32_t ks = (gk + j) % 3, kb = sK + ks * C::kTileBytes;
-                    if (j >= x.probe) {
+                    if (leader) {
+                        if (j >= probe) {
+                            const uint32_t acc = j > probe ? 1u : 0u, sc = tmem + col_s(j & 1);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_ts(tmem + kColDQ, tmem + col_s(j & 1) + ds_col(kk),
-                                    sdesc_sw128(kb + kk * 2048, C::kSlabBytes, 1024), C::kIdescDQ, (j > x.probe || kk > 0));
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_ts(tmem + kColDQ, sc + ds_col(kk), sdesc_sw128(kb + kk * 2048, C::kSlabBytes, 1024),
+                                        C::kIdescDQ, kk > 0 ? 1u : acc);
+                        }
+                        umma_commit(bar(B_K_EMPTY + ks));
                     }
-                    umma_commit(bar(B_K_EMPTY + ks));
+                    __syncwarp();
                     if (j + 2 < T && !issue_s(gk + j + 2, j & 1)) { stop = true; break; }
                 }
                 if (stop) break;
                 gk += T;
-                umma_commit(bar(B_DQ_DONE));
+                if (leader) umma_commit(bar(B_DQ_DONE));
+                __syncwarp();
             }
-            umma_commit(bar(B_MMA_DONE));
-            drain_bar(bar(B_MMA_DONE), 0, hdr, 246);
+            if (leader) {
+                umma_commit(bar(B_MMA_DONE));
+                drain_bar(bar(B_MMA_DONE), 0, hdr, 246);
+            }
         }
         __syncwarp();
     } else {
@@ -594,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw + C::oBar + 8 * B_COUNT);
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) {
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
 
     if (warp >= 8) {
         regs_dec<kRegsOther>();
@@ -671,76 +688,94 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nu > 0) drain_bar(bar(B_KV_FULL), (nu - 1) & 1, hdr, 265);
             for (uint32_t i = g >= 3 ? g - 3 : 0; i < g; ++i) drain_bar(bar(B_Q_FULL + i % 3), (i / 3) & 1, hdr, 266);
             for (uint32_t i = g >= 2 ? g - 2 : 0; i < g; ++i) drain_bar(bar(B_O_FULL + (i & 1)), (i >> 1) & 1, hdr, 267);
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9) {
             // ---------------------------------------------------------- MMA issue
+            // the whole warp walks the tiles, one elected lane issues (uniform descriptors)
+            const bool leader = elect_one();
             uint32_t g = 0, nu = 0;  // tiles, units with tiles
             bool stop = false;
             // column (from a buffer's first) of the bf16 pairs of rows 16 kk .. + 15: warpgroup
             // kk / 4 wrote its 64 rows over the first 32 columns of its own half
             auto pcol = [](int kk) { return 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3); };
             auto issue_dv = [&](uint32_t t, bool first) -> bool {  // dV += P^T dO of tile t
-                if (!wait_bar(bar(B_P_FULL), t & 1, abort, hdr, 268)) return false;
+                if (!wait_bar_warp(bar(B_P_FULL), t & 1, abort, hdr, 268)) return false;
                 tc_fence_after();
                 const uint32_t gb = sDO + (t & 1) * C::kTileBytes;
+                if (leader) {
+                    const uint32_t acc = first ? 0u : 1u;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
-                            C::kIdescAcc, (!first || kk > 0));
-                umma_commit(bar(B_O_EMPTY + (t & 1)));
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
+                                C::kIdescAcc, kk > 0 ? 1u : acc);
+                    umma_commit(bar(B_O_EMPTY + (t & 1)));
+                }
+                __syncwarp();
                 return true;
             };
             auto issue_dk = [&](uint32_t t, bool first) -> bool {  // dK += dS^T Q of tile t
-                if (!wait_bar(bar(B_DS_FULL), t & 1, abort, hdr, 269)) return false;
+                if (!wait_bar_warp(bar(B_DS_FULL), t & 1, abort, hdr, 269)) return false;
                 tc_fence_after();
                 const uint32_t qb = sQ + (t % 3) * C::kTileBytes;
+                if (leader) {
+                    const uint32_t acc = first ? 0u : 1u;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_ts(tmem + kColDK, tmem + kColDPT + pcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
-                            C::kIdescAcc, (!first || kk > 0));
-                umma_commit(bar(B_Q_EMPTY + t % 3));
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(tmem + kColDK, tmem + kColDPT + pcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
+                                C::kIdescAcc, kk > 0 ? 1u : acc);
+                    umma_commit(bar(B_Q_EMPTY + t % 3));
+                }
+                __syncwarp();
                 return true;
             };
-            // D[col] = A[sA] B[sB]^T over d
-            auto issue_ss = [&](uint32_t col, uint32_t sa, uint32_t sb) {
+            // D[col] = A[sA] B[sB]^T over d, then an arrival on `done`
+            auto issue_ss = [&](uint32_t col, uint32_t sa, uint32_t sb, uint32_t done) {
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
-                    umma_ss(tmem + col, sdesc_sw128(sa + off, 16, 1024), sdesc_sw128(sb + off, 16, 1024), C::kIdescSS, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kSlabBytes + (kk & 3) * 32;
+                        umma_ss(tmem + col, sdesc_sw128(sa + off, 16, 1024), sdesc_sw128(sb + off, 16, 1024), C::kIdescSS, kk > 0);
+                    }
+                    umma_commit(done);
                 }
+                __syncwarp();
             };
             for (int it = 0; !stop; ++it) {
                 const int slot = it & 1;
-                if (!wait_bar(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 270)) break;
-                const int u = sh.item[slot];
-                mbar_arrive(bar(B_ITEM_EMPTY + slot));
+                if (!wait_bar_warp(bar(B_ITEM_FULL + slot), (it >> 1) & 1, abort, hdr, 270)) break;
+                const int u = uniform(sh.item[slot]);
+                if (leader) mbar_arrive(bar(B_ITEM_EMPTY + slot));
+                __syncwarp();
                 if (u < 0) break;
                 Unit x;
                 decode(a, p, u, x);
-                if (x.i0 >= x.i1) continue;
-                if (!wait_bar(bar(B_KV_FULL), nu & 1, abort, hdr, 271)) break;
-                for (int i = x.i0; i < x.i1; ++i, ++g) {
-                    if (i == x.i0 + 1 && nu > 0 && !wait_bar(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 272)) { stop = true; break; }
-                    if (i > x.i0 && !issue_dv(g - 1, i - 1 == x.i0)) { stop = true; break; }
-                    if (!wait_bar(bar(B_Q_FULL + g % 3), (g / 3) & 1, abort, hdr, 273)) { stop = true; break; }
+                const int i0 = uniform(x.i0), i1 = uniform(x.i1);
+                if (i0 >= i1) continue;
+                if (!wait_bar_warp(bar(B_KV_FULL), nu & 1, abort, hdr, 271)) break;
+                for (int i = i0; i < i1; ++i, ++g) {
+                    if (i == i0 + 1 && nu > 0 && !wait_bar_warp(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 272)) { stop = true; break; }
+                    if (i > i0 && !issue_dv(g - 1, i - 1 == i0)) { stop = true; break; }
+                    if (!wait_bar_warp(bar(B_Q_FULL + g % 3), (g / 3) & 1, abort, hdr, 273)) { stop = true; break; }
                     tc_fence_after();
-                    issue_ss(kColST, sK, sQ + (g % 3) * C::kTileBytes);
-                    umma_commit(bar(B_S_FULL));
-                    if (i > x.i0 && !issue_dk(g - 1, i - 1 == x.i0)) { stop = true; break; }
-                    if (!wait_bar(bar(B_O_FULL + (g & 1)), (g >> 1) & 1, abort, hdr, 274)) { stop = true; break; }
+                    issue_ss(kColST, sK, sQ + (g % 3) * C::kTileBytes, bar(B_S_FULL));
+                    if (i > i0 && !issue_dk(g - 1, i - 1 == i0)) { stop = true; break; }
+                    if (!wait_bar_warp(bar(B_O_FULL + (g & 1)), (g >> 1) & 1, abort, hdr, 274)) { stop = true; break; }
                     tc_fence_after();
-                    issue_ss(kColDPT, sV, sDO + (g & 1) * C::kTileBytes);
-                    umma_commit(bar(B_DP_FULL));
+                    issue_ss(kColDPT, sV, sDO + (g & 1) * C::kTileBytes, bar(B_DP_FULL));
                 }
                 if (stop) break;
-                umma_commit(bar(B_KV_EMPTY));
-                const bool one = x.i1 - x.i0 == 1;
-                if (one && nu > 0 && !wait_bar(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 275)) break;
+                if (leader) umma_commit(bar(B_KV_EMPTY));
+                __syncwarp();
+                const bool one = i1 - i0 == 1;
+                if (one && nu > 0 && !wait_bar_warp(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 275)) break;
                 if (!issue_dv(g - 1, one) || !issue_dk(g - 1, one)) break;
-                umma_commit(bar(B_ACC_DONE));
+                if (leader) umma_commit(bar(B_ACC_DONE));
+                __syncwarp();
                 ++nu;
             }
-            umma_commit(bar(B_MMA_DONE));
-            drain_bar(bar(B_MMA_DONE), 0, hdr, 276);
+            if (leader) {
+                umma_commit(bar(B_MMA_DONE));
+                drain_bar(bar(B_MMA_DONE), 0, hdr, 276);
+            }
         }
         __syncwarp();
     } else {
