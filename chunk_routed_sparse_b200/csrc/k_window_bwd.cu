@@ -393,36 +393,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b = j & 1;
                 if (!wait_bar_warp(bar(B_S_FULL + b), (b ? ns[1] : ns[0]) & 1, abort, hdr, 252)) { stop = true; break; }
                 if (b) ++ns[1]; else ++ns[0];
-                if (!wait_bar_warp(bar(B_DP_FULL), gt & 1, abort, hdr, 253)) { stop = true; break; }
                 tc_fence_after();
                 const uint32_t s_addr = lane_addr + col_s(b) + 64 * wg, p_addr = lane_addr + kColDP + 64 * wg;
                 const int k0 = key0 + 64 * wg;
                 const int nsk = min(vis.s, end) - k0, lo = vis.lo - k0, hi = min(vis.hi, end) - k0;
-                if (!__all_sync(0xffffffffu, !live || nsk >= 64 || (lo <= 0 && hi >= 64))) {
-                    // masked scores and their dP (which a key past the lengths may have made NaN), in TMEM
+                const bool masked = !__all_sync(0xffffffffu, !live || nsk >= 64 || (lo <= 0 && hi >= 64));
+                if (masked) {
 #pragma unroll 1
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t keep = win::bits(0, nsk - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w);
-                        mask_cols(s_addr + 32 * w, keep, kMinusInf);
-                        mask_cols(p_addr + 32 * w, keep, 0u);
-                    }
+                    for (int w = 0; w < 2; ++w)
+                        mask_cols(s_addr + 32 * w, win::bits(0, nsk - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w), kMinusInf);
                     tmem_wait_st();
                 }
-                uint32_t s[64], p[64];
+                // p while dP is still being formed
+                uint32_t s[64];
                 tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                 tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                tmem_ld32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
-                tmem_ld32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
                 tmem_wait_ld_regs(s);
-                tmem_wait_ld_regs(p);
+#pragma unroll
+                for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c]), sl2, -lse2)));
+                if (!wait_bar_warp(bar(B_DP_FULL), gt & 1, abort, hdr, 253)) { stop = true; break; }
+                tc_fence_after();
+                if (masked) {  // dP of a key past the lengths may be NaN
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w)
+                        mask_cols(p_addr + 32 * w, win::bits(0, nsk - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w), 0u);
+                    tmem_wait_st();
+                }
                 uint32_t pk[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float d0 = ex2(fmaf(__uint_as_float(s[2 * c]), sl2, -lse2)) * (__uint_as_float(p[2 * c]) - drow);
-                    const float d1 = ex2(fmaf(__uint_as_float(s[2 * c + 1]), sl2, -lse2)) * (__uint_as_float(p[2 * c + 1]) - drow);
-                    if (c & 1) rb = f2_add(rb, f2_pack(d0, d1));
-                    else ra = f2_add(ra, f2_pack(d0, d1));
-                    pk[c] = pack_bf16(d0, d1);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+                    tmem_ld32(p_addr + 32 * h, p);
+                    tmem_wait_ld_regs(p);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float d0 = __uint_as_float(s[32 * h + 2 * c]) * (__uint_as_float(p[2 * c]) - drow);
+                        const float d1 = __uint_as_float(s[32 * h + 2 * c + 1]) * (__uint_as_float(p[2 * c + 1]) - drow);
+                        if (c & 1) rb = f2_add(rb, f2_pack(d0, d1));
+                        else ra = f2_add(ra, f2_pack(d0, d1));
+                        pk[16 * h + c] = pack_bf16(d0, d1);
+                    }
                 }
                 tmem_st32(s_addr, pk);
                 if (end - key0 < 128) {  // K rows past the tile's keys: zeros (S has read them)
