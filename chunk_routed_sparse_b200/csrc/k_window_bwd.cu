@@ -130,7 +130,7 @@ struct Cfg {
 
 enum {
     B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 7, B_V_FULL = 10, B_V_EMPTY = 12, B_QDO_FULL = 14,
-    B_QDO_EMPTY = 15, B_S_FULL = 16, B_DP_FULL = 18, B_DS_FULL = 19, B_DQ_DONE = 20, B_MMA_DONE = 21, B_SUM = 22, B_COUNT = 23
+    B_QDO_EMPTY = 15, B_S_FULL = 16, B_DP_FULL = 18, B_DS_FULL = 19, B_DQ_DONE = 20, B_MMA_DONE = 21, B_SUM = 22, B_DP_READ = 23, B_COUNT = 24
 };
 static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < B_COUNT; ++x) {
             int n = 1;
             if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256;
-            if (x == B_DS_FULL || x == B_SUM) n = 256;
+            if (x == B_DS_FULL || x == B_SUM || x == B_DP_READ) n = 256;
             mbar_init(bar(x), n);
         }
         sh.abort = 0;
@@ -312,11 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (T == 1 && leader) umma_commit(bar(B_QDO_EMPTY));
                 __syncwarp();
                 for (int j = 0; j < T; ++j) {
+                    // dP(j) is in the warps' registers: dP(j + 1) runs while they form dS(j)
+                    if (!wait_bar_warp(bar(B_DP_READ), gt & 1, abort, hdr, 247)) { stop = true; break; }
+                    tc_fence_after();
+                    if (j + 1 < T && !issue_dp()) { stop = true; break; }
+                    if (T > 1 && j == T - 2 && leader) umma_commit(bar(B_QDO_EMPTY));  // the last S was issued before it
                     if (!wait_bar_warp(bar(B_DS_FULL), gt & 1, abort, hdr, 245)) { stop = true; break; }
                     tc_fence_after();
                     ++gt;
-                    if (j + 1 < T && !issue_dp()) { stop = true; break; }
-                    if (T > 1 && j == T - 2 && leader) umma_commit(bar(B_QDO_EMPTY));  // the last S was issued before it
                     const uint32_t ks = (gk + j) % 3, kb = sK + ks * C::kTileBytes;
                     if (leader) {
                         if (j >= probe) {
@@ -419,20 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mask_cols(p_addr + 32 * w, win::bits(0, nsk - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w), 0u);
                     tmem_wait_st();
                 }
-                uint32_t pk[32];
+                uint32_t p[64], pk[32];
+                tmem_ld32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+                tmem_ld32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
+                tmem_wait_ld_regs(p);
+                tc_fence_before();
+                mbar_arrive(bar(B_DP_READ));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-                    tmem_ld32(p_addr + 32 * h, p);
-                    tmem_wait_ld_regs(p);
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float d0 = __uint_as_float(s[32 * h + 2 * c]) * (__uint_as_float(p[2 * c]) - drow);
-                        const float d1 = __uint_as_float(s[32 * h + 2 * c + 1]) * (__uint_as_float(p[2 * c + 1]) - drow);
-                        if (c & 1) rb = f2_add(rb, f2_pack(d0, d1));
-                        else ra = f2_add(ra, f2_pack(d0, d1));
-                        pk[16 * h + c] = pack_bf16(d0, d1);
-                    }
+                for (int c = 0; c < 32; ++c) {
+                    const float d0 = __uint_as_float(s[2 * c]) * (__uint_as_float(p[2 * c]) - drow);
+                    const float d1 = __uint_as_float(s[2 * c + 1]) * (__uint_as_float(p[2 * c + 1]) - drow);
+                    if (c & 1) rb = f2_add(rb, f2_pack(d0, d1));
+                    else ra = f2_add(ra, f2_pack(d0, d1));
+                    pk[c] = pack_bf16(d0, d1);
                 }
                 tmem_st32(s_addr, pk);
                 if (end - key0 < 128) {  // K rows past the tile's keys: zeros (S has read them)
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // S^T(i) runs as soon as dV(i-1) has read P^T(i-1) in its columns, while ds(i-1) is
 // formed; the exponentials of tile i run under dK(i-1) and dP^T(i). (All four products
 // of a tile in a row, then its math: 2.80 ms on the single-shot training step against
-// 2.15 ms; two TMEM buffers of 64 rows each: 3.14 ms, a 64-column product takes as
+// 1.97 ms; two TMEM buffers of 64 rows each: 3.14 ms, a 64-column product takes as
 // long as a 128-column one.)
 //   warp 8 (one lane): units and TMA: K and V of a unit, Q tiles into a 3-stage ring,
 //          dO tiles and row statistics into a 2-stage ring.
@@ -541,7 +543,7 @@ struct Cfg {
 enum {
     B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_KV_FULL = 4, B_KV_EMPTY = 5, B_Q_FULL = 6, B_Q_EMPTY = 9, B_O_FULL = 12,
     B_O_EMPTY = 14, B_S_FULL = 16, B_P_FULL = 17, B_DP_FULL = 18, B_DS_FULL = 19, B_ACC_DONE = 20, B_EPI_DONE = 21,
-    B_MMA_DONE = 22, B_TAIL = 23, B_COUNT = 25
+    B_MMA_DONE = 22, B_TAIL = 23, B_P_HALF = 25, B_COUNT = 26
 };
 static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 
@@ -628,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 1;
             if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256;
             if (x == B_O_EMPTY || x == B_O_EMPTY + 1) n = 1 + 256;  // dV has read dO, the warps the statistics
-            if (x == B_P_FULL || x == B_DS_FULL || x == B_EPI_DONE) n = 256;
+            if (x == B_P_FULL || x == B_P_HALF || x == B_DS_FULL || x == B_EPI_DONE) n = 256;
             if (x == B_TAIL || x == B_TAIL + 1) n = 128;
             mbar_init(bar(x), n);
         }
@@ -708,15 +710,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             // kk / 4 wrote its 64 rows over the first 32 columns of its own half
             auto pcol = [](int kk) { return 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3); };
             auto issue_dv = [&](uint32_t t, bool first) -> bool {  // dV += P^T dO of tile t
-                if (!wait_bar_warp(bar(B_P_FULL), t & 1, abort, hdr, 268)) return false;
-                tc_fence_after();
                 const uint32_t gb = sDO + (t & 1) * C::kTileBytes;
+                const uint32_t acc = first ? 0u : 1u;
+                // the first 32 rows of either warpgroup, then the others
+                if (!wait_bar_warp(bar(B_P_HALF), t & 1, abort, hdr, 277)) return false;
+                tc_fence_after();
                 if (leader) {
-                    const uint32_t acc = first ? 0u : 1u;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
-                                C::kIdescAcc, kk > 0 ? 1u : acc);
+                        if ((kk & 2) == 0)
+                            umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
+                                    C::kIdescAcc, kk > 0 ? 1u : acc);
+                }
+                __syncwarp();
+                if (!wait_bar_warp(bar(B_P_FULL), t & 1, abort, hdr, 268)) return false;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        if ((kk & 2) != 0)
+                            umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
+                                    C::kIdescAcc, 1u);
                     umma_commit(bar(B_O_EMPTY + (t & 1)));
                 }
                 __syncwarp();
@@ -862,10 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s[32 * c + 2 * e + 1] = __float_as_uint(p1f);
                     }
                     tmem_st16(s_addr + 16 * c, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar(c == 0 ? B_P_HALF : B_P_FULL));
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar(B_P_FULL));
                 if (!wait_bar_warp(bar(B_DP_FULL), g & 1, abort, hdr, 285)) { stop = true; break; }
                 tc_fence_after();
                 if (n < kTile) {  // dP^T of a row past the last may be NaN

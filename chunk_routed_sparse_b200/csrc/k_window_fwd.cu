@@ -5,14 +5,15 @@
 //   (window.cuh), lse_t = log sum_u exp(scale q_t . k_u);
 //   a row that sees no key: O = 0, lse = -inf.
 //
-// One persistent CTA per SM walks work items (256 consecutive rows of a head, two
+// One persistent CTA per SM walks work items (up to 256 consecutive rows of a head, two
 // 128-row tiles A and B that share one key stream) in a fixed order: no counter in
 // memory, so calls on different streams and captured graphs share nothing.
 //   warp 8 (one lane): TMA of Q tiles and of 128-key K and V tiles (2-stage rings).
 //   warp 9 (one lane): S_q = Q K^T and O_q += P V (P from TMEM), alternating A and
 //          B; an item's last PV and the next item's first S are issued back to back.
 //   warps 0-3 / 4-7: softmax of tile A / B, one thread a row, running max and sum
-//          in fp32, P written over S as bf16 (a rounding of 2^-9 of each weight; the
+//          in fp32, P written over S as bf16 in two halves, so that the first half of
+//          P V runs under the second half's exponentials (a rounding of 2^-9 of each weight; the
 //          sum is of the unrounded weights); the epilogue stages O through shared
 //          memory into whole 128-byte row pieces.
 // A tile that one of A, B cannot see is skipped for it; a tile that every row of a
@@ -20,7 +21,7 @@
 // their scores become -inf and their V rows are zeroed in shared memory (0 x NaN).
 // Every wait is bounded (2 s): a wait that gives up records itself in the error
 // word of moc_window_device_error and every role leaves.
-#include <mutex>
+#include <atomic>
 
 #include "common.cuh"
 #include "pipeline.cuh"
@@ -34,9 +35,7 @@ namespace {
 __device__ int32_t g_window_err[64];  // error code and detail of the window kernels on this device
 
 constexpr int kMaxDevices = 64;
-int32_t* g_err_ptr[kMaxDevices];
-cudaError_t g_err_status[kMaxDevices];
-std::once_flag g_err_once[kMaxDevices];
+std::atomic<int32_t*> g_err_ptr[kMaxDevices];  // its address on each device, looked up once
 
 }  // namespace
 
@@ -45,13 +44,14 @@ cudaError_t window_error_word(int32_t** word) {
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    std::call_once(g_err_once[dev], [dev] {
-        void* p = nullptr;
-        g_err_status[dev] = cudaGetSymbolAddress(&p, g_window_err);
-        g_err_ptr[dev] = static_cast<int32_t*>(p);
-    });
-    *word = g_err_ptr[dev];
-    return g_err_status[dev];
+    *word = g_err_ptr[dev].load(std::memory_order_acquire);
+    if (*word) return cudaSuccess;
+    void* p = nullptr;
+    const cudaError_t st = cudaGetSymbolAddress(&p, g_window_err);
+    if (st != cudaSuccess) return st;
+    *word = static_cast<int32_t*>(p);
+    g_err_ptr[dev].store(*word, std::memory_order_release);
+    return cudaSuccess;
 }
 
 namespace {
@@ -59,7 +59,6 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 384;
-constexpr int kRowsItem = 256;
 // launched at 168 registers a thread (384 x 168 = 64512): softmax warpgroups 216,
 // the loading / issuing one 72: 2 x 128 x 216 + 128 x 72 = 64512
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
@@ -88,13 +87,13 @@ __device__ __forceinline__ uint32_t col_o(int q) { return q ? 384u : 256u; }
 
 enum {
     B_Q_FULL = 0, B_Q_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 6, B_V_FULL = 8, B_V_EMPTY = 10, B_S_FULL = 12,
-    B_P_FULL = 14, B_PV_DONE = 16, B_MMA_DONE = 18, B_COUNT = 19
+    B_P_FULL = 14, B_PV_DONE = 16, B_MMA_DONE = 18, B_P_HALF = 19, B_COUNT = 21
 };
-struct Shared {  // at oBar + 160
+struct Shared {  // at oBar + 176
     uint32_t tmem_base;
     int abort;
 };
-static_assert(B_COUNT * 8 <= 160, "barriers");
+static_assert(B_COUNT * 8 <= 176, "barriers");
 
 // An item, and one of its two row tiles. Each role keeps the tiles in scalars (an
 // index that the compiler cannot see through would put them in local memory).
@@ -114,14 +113,15 @@ struct QTile {
 
 // Items of one position range lie next to each other over the heads; the last rows
 // (the longest spans under an open causal window) come first.
-__device__ __forceinline__ void decode(const WinArgs& a, int nqt, int item, Item& x) {
+__device__ __forceinline__ void decode(const WinArgs& a, int rows, int item, Item& x) {
+    const int nqt = (a.Lq + rows - 1) / rows;
     const int heads = a.B * a.Hq;
     const int qt = nqt - 1 - item / heads, bh = item % heads;
     x.b = bh / a.Hq;
     x.hq = bh - x.b * a.Hq;
-    x.t0 = qt * kRowsItem;
+    x.t0 = qt * rows;
     x.seq = win::seq(a, x.b);
-    x.end = min(x.t0 + kRowsItem, x.seq.m);
+    x.end = min(x.t0 + rows, x.seq.m);
     x.all = win::Span{0, 0, 0, 0, 0};
     if (x.end > x.t0) x.all = win::span(a, x.seq, x.t0, x.end);
     x.tiles = x.all.na + x.all.nb;
@@ -149,7 +149,7 @@ __device__ __forceinline__ int nth_item(int k) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WinArgs a, int n_items, int nqt,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WinArgs a, int n_items, int rows_item,
                       __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -157,14 +157,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
     const uint32_t sQ = base + C::oQ, sK = base + C::oK, sV = base + C::oV, sBar = base + C::oBar;
-    Shared& sh = *reinterpret_cast<Shared*>(gbase + C::oBar + 160);
+    Shared& sh = *reinterpret_cast<Shared*>(gbase + C::oBar + 176);
     volatile int* abort = &sh.abort;
     int32_t* const hdr = g_window_err;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
-        for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1) ? 128 : 1);
+        for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1 || x >= B_P_HALF) ? 128 : 1);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int item = nth_item(k);
                 if (item >= n_items) continue;
                 Item x;
-                decode(a, nqt, item, x);
+                decode(a, rows_item, item, x);
                 const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
                 const int qrow = (x.b * a.Hq + x.hq) * a.Lq + x.t0;
                 const int krow = (x.b * a.Hk + x.hq / a.group) * a.Lk;
@@ -249,13 +249,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool stop = false;
             // O_q += P_q V of the previous key tile
             auto issue_pv = [&](const int q) -> bool {
-                if (!wait_bar_warp(bar(B_P_FULL + q), (np[q] - 1) & 1, abort, hdr, 211)) return false;
+                if (!wait_bar_warp(bar(B_P_HALF + q), (np[q] - 1) & 1, abort, hdr, 210)) return false;
                 tc_fence_after();
                 const uint32_t vb = sV + ((gt - 1) & 1) * C::kTileBytes;
                 const uint32_t acc = fresh[q] ? 0u : 1u;
                 if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_ts(tmem + col_o(q), tmem + col_s(q) + kk * 8, sdesc_sw128(vb + kk * 2048, C::kSlabBytes, 1024),
+                                C::kIdescPV, kk > 0 ? 1u : acc);
+                }
+                __syncwarp();
+                if (!wait_bar_warp(bar(B_P_FULL + q), (np[q] - 1) & 1, abort, hdr, 211)) return false;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int kk = 4; kk < 8; ++kk)
                         umma_ts(tmem + col_o(q), tmem + col_s(q) + kk * 8, sdesc_sw128(vb + kk * 2048, C::kSlabBytes, 1024),
                                 C::kIdescPV, kk > 0 ? 1u : acc);
                     umma_commit(bar(B_PV_DONE + q));
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int item = nth_item(k);
                 if (item >= n_items) continue;
                 Item x;
-                decode(a, nqt, item, x);
+                decode(a, rows_item, item, x);
                 const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
                 const int tiles = uniform(x.tiles);
                 bool have[2] = {false, false};
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int item = nth_item(k);
             if (item >= n_items) continue;
             Item x;
-            decode(a, nqt, item, x);
+            decode(a, rows_item, item, x);
             const QTile qt = tile_of(a, x, q);
             if (qt.rows == 0) {
                 gt += x.tiles;
@@ -362,20 +371,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int ns = min(vis.s, end) - key0, lo = vis.lo - key0, hi = min(vis.hi, end) - key0;
                 if (!__all_sync(0xffffffffu, !live || ns >= 128 || (lo <= 0 && hi >= 128))) {
-                    // masked in TMEM, 32 columns at a time, before the scores are loaded: masking
-                    // them among the 128 loaded registers spilled in every tile (1.42 ms against
-                    // 0.80 ms on the single-shot clip)
+                    // masked in TMEM, 64 columns at a time, before the scores are loaded: masking
+                    // them among the 128 loaded registers spilled in every tile (1.09 ms against
+                    // 0.71 ms on the single-shot clip)
 #pragma unroll 1
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t keep = win::bits(0, ns - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w);
-                        if (__all_sync(0xffffffffu, keep == 0xffffffffu)) continue;
-                        uint32_t v[32];
-                        tmem_ld32(s_addr + w * 32, v);
+                    for (int w = 0; w < 128; w += 64) {
+                        const uint32_t k0 = win::bits(0, ns - w) | win::bits(lo - w, hi - w);
+                        const uint32_t k1 = win::bits(0, ns - w - 32) | win::bits(lo - w - 32, hi - w - 32);
+                        if (__all_sync(0xffffffffu, (k0 & k1) == 0xffffffffu)) continue;
+                        uint32_t v[64];
+                        tmem_ld32(s_addr + w, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                        tmem_ld32(s_addr + w + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
                         tmem_wait_ld_regs(v);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(keep & (1u << c))) v[c] = 0xff800000u;  // -inf
-                        tmem_st32(s_addr + w * 32, v);
+                        for (int c = 0; c < 64; ++c)
+                            if (!((c < 32 ? k0 : k1) & (1u << (c & 31)))) v[c] = 0xff800000u;  // -inf
+                        tmem_st32(s_addr + w, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                        tmem_st32(s_addr + w + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
                     }
                     tmem_wait_st();
                 }
@@ -415,6 +427,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st32(o_addr + c * 32, o);
                     }
                 }
+                if (end - key0 < 128) {  // V rows past the tile's keys: zeros, whatever was loaded
+                    if (!wait_bar_warp(bar(B_V_FULL + (gt & 1)), (gt >> 1) & 1, abort, hdr, 223)) { stop = true; break; }
+                    if (row >= end - key0) {
+                        const uint32_t vr = sV + (gt & 1) * C::kTileBytes + row * 128;
+#pragma unroll
+                        for (int i = 0; i < C::kSlabs * 8; ++i)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vr + (i >> 3) * C::kSlabBytes + (i & 7) * 16),
+                                         "r"(0u) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                }
                 // a row without a visible key so far: its weights are exp2(-inf - 0) = 0
                 const float m0 = m_used > -INFINITY ? m_used : 0.f;
                 const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m0, -m0);
@@ -433,22 +456,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[c] = pack_bf16(p0, p1);
                     }
                     tmem_st32(s_addr + h * 32, pk);
+                    if (h == 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(bar(B_P_HALF + q));
+                    }
                 }
                 float r0, r1, r2, r3;
                 f2_unpack(sum2a, r0, r1);
                 f2_unpack(sum2b, r2, r3);
                 l = l * alpha + ((r0 + r1) + (r2 + r3));
-                if (end - key0 < 128) {  // V rows past the tile's keys: zeros, whatever was loaded
-                    if (!wait_bar_warp(bar(B_V_FULL + (gt & 1)), (gt >> 1) & 1, abort, hdr, 223)) { stop = true; break; }
-                    if (row >= end - key0) {
-                        const uint32_t vr = sV + (gt & 1) * C::kTileBytes + row * 128;
-#pragma unroll
-                        for (int i = 0; i < C::kSlabs * 8; ++i)
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vr + (i >> 3) * C::kSlabBytes + (i & 7) * 16),
-                                         "r"(0u) : "memory");
-                    }
-                    fence_proxy_async_smem();
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(B_P_FULL + q));
@@ -522,10 +539,17 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int nqt = (a.Lq + kRowsItem - 1) / kRowsItem;
-    const int n_items = a.B * a.Hq * nqt;
+    // Two row tiles an item keep the tensor core busy and share their keys; while that
+    // leaves half of the SMs without an item, one tile each ends sooner (the tiny scene,
+    // 18 items or 34: 18.3 against 14.5 us).
+    int rows_item = 256;
+    int n_items = a.B * a.Hq * ((a.Lq + rows_item - 1) / rows_item);
+    if (2 * n_items <= sms) {
+        rows_item = 128;
+        n_items = a.B * a.Hq * ((a.Lq + rows_item - 1) / rows_item);
+    }
     window_fwd_kernel<D><<<n_items < sms ? n_items : sms, kThreads, smem, s>>>(
-        tmQ, tmK, tmV, a, n_items, nqt, static_cast<__nv_bfloat16*>(O), lse);
+        tmQ, tmK, tmV, a, n_items, rows_item, static_cast<__nv_bfloat16*>(O), lse);
     return cudaGetLastError();
 }
 

@@ -11,7 +11,8 @@ bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 constexpr int64_t kMaxLen = int64_t(1) << 28;   // positions and their differences with a limit of 2^30 fit 32 bits
-constexpr int64_t kMaxRows = int64_t(1) << 31;  // rows of one tensor: a copy's row coordinate is 32 bits
+// rows of one tensor: a copy's row coordinate, and an item past the last, fit 32 bits
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 65536;
 
 moc_status make_args(moc::WinArgs& a, int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, int64_t left,
                      int64_t right, int64_t sinks, int causal, const int32_t* q_len, const int32_t* kv_len,

@@ -48,7 +48,7 @@ class Rope:
                  original_length: float = 0.0, alpha: float = 1.0, beta: float = 32.0,
                  attention_factor: Optional[float] = None):
         axes = (int(dim),) if axes is None else tuple(int(a) for a in axes)
-        if sum(axes) != dim:
+        if any(abs(a) >= 1 << 31 for a in axes) or sum(axes) != dim:
             raise ValueError(f"axes {axes} do not sum to {dim} rotated dims")
         if scaling not in SCALING:
             raise ValueError(f"unknown scaling {scaling!r}: one of {', '.join(SCALING)}")

@@ -50,6 +50,12 @@ def _problem(Q, K, V, q_len, kv_len):
     return B, Hq, Hk, Lq, Lk, d
 
 
+def _limits(left, right, sinks):
+    """The window's sizes in 64 bits: any negative limit is none, any huge one reaches every key."""
+    far = 1 << 40
+    return max(min(int(left), far), -1), max(min(int(right), far), -1), max(min(int(sinks), far), -1)
+
+
 def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, causal: bool = False,
                          q_len: Optional[torch.Tensor] = None, kv_len: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, O: Optional[torch.Tensor] = None,
@@ -57,6 +63,7 @@ def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 
     """(O, lse) (moc_window_attention). Rows past q_len are left as they were in a
     given O or lse, and are 0 and -inf in new ones."""
     B, Hq, Hk, Lq, Lk, d = _problem(Q, K, V, q_len, kv_len)
+    left, right, sinks = _limits(left, right, sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if O is None:
         O = torch.empty_like(Q) if q_len is None else torch.zeros_like(Q)
@@ -81,6 +88,7 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
     """(dQ, dK, dV) for the upstream gradient dO (moc_window_attention_bwd). Rows past
     the lengths are left as they were in given tensors and are 0 in new ones."""
     B, Hq, Hk, Lq, Lk, d = _problem(Q, K, V, q_len, kv_len)
+    left, right, sinks = _limits(left, right, sinks)
     _tensor("O", O, Q.shape, Q.device)
     _tensor("dO", dO, Q.shape, Q.device)
     _tensor("lse", lse, (B, Hq, Lq), Q.device, torch.float32)

@@ -529,7 +529,7 @@ moc_status moc_qk_norm_rope_bwd(const moc_rope* rope, int dtype, int B, int Hq, 
  * that no row sees are not read into any result, whatever they hold. (A key
  * that only some rows of 256 see, and that holds an infinity or a NaN, can reach
  * the others as 0 x infinity.) softmax_scale > 0, finite. Lq, Lk < 2^28,
- * B Hq Lq and B Hk Lk < 2^31, B and Hq at most 65535. Asynchronous, no
+ * B Hq Lq and B Hk Lk < 2^31 - 65536, B and Hq at most 65535. Asynchronous, no
  * workspace; a device-side wait that gives up is reported by
  * moc_window_device_error. */
 moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q, const void* K,
