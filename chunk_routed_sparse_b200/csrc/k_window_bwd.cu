@@ -130,7 +130,7 @@ struct Cfg {
 
 enum {
     B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 7, B_V_FULL = 10, B_V_EMPTY = 12, B_QDO_FULL = 14,
-    B_QDO_EMPTY = 15, B_S_FULL = 16, B_DP_FULL = 18, B_DS_FULL = 19, B_DQ_DONE = 20, B_MMA_DONE = 21, B_SUM = 22, B_DP_READ = 23, B_COUNT = 24
+    B_QDO_EMPTY = 15, B_S_FULL = 16, B_DP_FULL = 18, B_DS_FULL = 19, B_DQ_DONE = 21, B_MMA_DONE = 22, B_SUM = 23, B_DP_READ = 24, B_COUNT = 25
 };
 static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < B_COUNT; ++x) {
             int n = 1;
             if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256;
-            if (x == B_DS_FULL || x == B_SUM || x == B_DP_READ) n = 256;
+            if (x == B_DS_FULL || x == B_DS_FULL + 1 || x == B_SUM || x == B_DP_READ) n = 256;
             mbar_init(bar(x), n);
         }
         sh.abort = 0;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     if (j + 1 < T && !issue_dp()) { stop = true; break; }
                     if (T > 1 && j == T - 2 && leader) umma_commit(bar(B_QDO_EMPTY));  // the last S was issued before it
-                    if (!wait_bar_warp(bar(B_DS_FULL), gt & 1, abort, hdr, 245)) { stop = true; break; }
+                    if (!wait_bar_warp(bar(B_DS_FULL + (gt & 1)), (gt >> 1) & 1, abort, hdr, 245)) { stop = true; break; }
                     tc_fence_after();
                     ++gt;
                     const uint32_t ks = (gk + j) % 3, kb = sK + ks * C::kTileBytes;
@@ -449,7 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_DS_FULL));
+                // a barrier for even tiles and one for odd: a warpgroup may be a tile ahead (its S
+                // and dP need nothing of this tile's dS), and must not complete this tile's phase
+                mbar_arrive(bar(B_DS_FULL + (gt & 1)));
                 ++gt;
             }
             if (stop) break;
