@@ -254,18 +254,29 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
     constexpr int LPR = D / 8, TPC = kThreads / LPR;
     __shared__ uint64_t turn[kMaxRopePairs];
     __shared__ uint8_t axis[kMaxRopePairs];
-    tab_to_smem(a, turn, axis);
     const int r = threadIdx.x % LPR, e0 = 8 * r;
     const int64_t tok = int64_t(blockIdx.x) * TPC + threadIdx.x / LPR;
     const bool live = tok < a.tokens;  // lanes past the last token work on it again and store nothing
     const int t = live ? int(tok) : a.tokens - 1;
     const int b = t / a.L, l = t - b * a.L;
+    const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
+    // the CTA's first rows are requested before the angles are formed
+    int k0 = 0, base = 0;
+    while (h_lo >= base + a.sec[k0].H) base += a.sec[k0++].H;
+    Raw<T> raw[kRows];
+    {
+        const RowSec& sec = a.sec[k0];
+        const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0 + (h_lo - base) * sec.xs[1];
+        const int n = min(h_hi - h_lo, sec.H - (h_lo - base));
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (u < n) load_raw<T, AL>(x + u * sec.xs[1], raw[u]);
+    }
+    tab_to_smem(a, turn, axis);
     Trig<HALF> tr;
     trig<HALF>(a, turn, axis, b, l, e0, tr);
-    const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
-    int base = 0;
 #pragma unroll 1
-    for (int k = 0; k < 3; ++k) {
+    for (int k = k0; k < 3; ++k) {
         const RowSec& sec = a.sec[k];
         const int lo = max(h_lo - base, 0), hi = min(h_hi - base, sec.H);
         base += sec.H;
@@ -279,10 +290,11 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
         }
 #pragma unroll 1
         for (int h = lo; h < hi; h += kRows) {
-            Raw<T> raw[kRows];
+            if (k > k0 || h > lo) {
 #pragma unroll
-            for (int u = 0; u < kRows; ++u)
-                if (h + u < hi) load_raw<T, AL>(x + (h + u) * sec.xs[1], raw[u]);
+                for (int u = 0; u < kRows; ++u)
+                    if (h + u < hi) load_raw<T, AL>(x + (h + u) * sec.xs[1], raw[u]);
+            }
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 if (h + u >= hi) break;
@@ -414,6 +426,7 @@ __global__ void __launch_bounds__(1024) rows_dw_kernel(int ctas, int D, const fl
     W* out = blockIdx.y == 0 ? dwq : dwk;
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
+#pragma unroll 8
     for (int i = threadIdx.y; i < ctas; i += 32) s += part[(size_t(i) * 2 + blockIdx.y) * D + c];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();

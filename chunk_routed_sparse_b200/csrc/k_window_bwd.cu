@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u < 0) break;
             Unit x;
             decode(a, nqt, u, x);
-            if (x.rows <= 0) continue;
+            const int rows_out = a.fill ? min(kTile, a.Lq - x.t0) : x.rows;  // with those past the last
+            if (rows_out <= 0) continue;
             const bool live = row < x.rows;
             const size_t rowg = (size_t(x.b) * a.Hq + x.hq) * size_t(a.Lq) + size_t(x.t0) + row;
             float2* my = stats + stat_row(a, int64_t(x.b) * a.Hq + x.hq) + x.t0 + row;
@@ -472,13 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(lane_addr + kColDQ + wg * HC + c0, o);
                     tmem_wait_ld_regs(o);
                 }
-                if (live) {
+                if (row < rows_out) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            w[e] = x.tiles > 0 ? pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * a.scale,
+                            w[e] = x.tiles > 0 && live ? pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * a.scale,
                                                            __uint_as_float(o[8 * i + 2 * e + 1]) * a.scale)
                                                : 0u;
                         *reinterpret_cast<uint4*>(dst + c0 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -820,7 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u < 0) break;
             Unit x;
             decode(a, p, u, x);
-            if (x.nk <= 0 && x.part < 0) continue;
+            const int keys_out = a.fill ? min(kTile, a.Lk - x.k0) : x.nk;  // with those past the last
+            if (keys_out <= 0 && x.part < 0) continue;
             // positions that see this thread's key: [v_lo, v_hi)
             const int key = x.k0 + row;
             int v_lo = key < a.sinks ? -(1 << 30) : key - a.right;
@@ -939,13 +941,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
                             reinterpret_cast<float4*>(dst)[i] = v;
                         }
-                    } else if (valid) {
+                    } else if (row < keys_out) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                w[e] = some ? pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * mul, __uint_as_float(o[8 * i + 2 * e + 1]) * mul) : 0u;
+                                w[e] = some && valid ? pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * mul, __uint_as_float(o[8 * i + 2 * e + 1]) * mul) : 0u;
                             *reinterpret_cast<uint4*>(out + orow + c0 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
@@ -979,7 +981,7 @@ __global__ void __launch_bounds__(256) window_dkv_join_kernel(const __grid_const
         const int c = int(i % PER), r = int(i / PER % 128), t = int(i / PER / 128 % 2);
         const int64_t tile = i / PER / 128 / 2;  // key tile x heads + (batch, key head)
         const int kt = int(tile / heads), bh = int(tile % heads), key = kt * kTile + r;
-        if (key >= win::seq(a, bh / a.Hk).n) continue;
+        if (key >= (a.fill ? a.Lk : win::seq(a, bh / a.Hk).n)) continue;
         const float4* src = reinterpret_cast<const float4*>(parts + ((tile * p.splits * 2 + t) * 128 + r) * D) + c;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < p.splits; ++k) {

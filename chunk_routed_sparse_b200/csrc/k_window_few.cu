@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads)
             v = fmaf(f, po[k], v);
             l = fmaf(f, pl[k], l);
         }
-        if (t >= seq.m) continue;  // rows past the last stay as they were
+        if (t >= seq.m && !a.fill) continue;  // rows past the last stay as they were
         const bool seen = l > 0.f || l != l;  // NaN stays NaN
         O[(qrow + r) * D + c] = __float2bfloat16_rn(seen ? v / l : 0.f);
         if (c == 0 && lse) lse[qrow + r] = seen ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;

@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item x;
             decode(a, rows_item, item, x);
             const QTile qt = tile_of(a, x, q);
-            if (qt.rows == 0) {
+            // rows to write: the live ones, and with a.fill those past the last
+            const int rows_out = a.fill ? min(128, min(a.Lq, x.t0 + rows_item) - x.t0 - 128 * q) : qt.rows;
+            if (rows_out <= 0) {
                 gt += x.tiles;
                 continue;
             }
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_bar_warp(bar(B_PV_DONE + q), (np - 1) & 1, abort, hdr, 224)) break;
                 tc_fence_after();
             }
-            const bool seen = l > 0.f || l != l;  // NaN stays NaN
+            const bool seen = live && (l > 0.f || l != l);  // NaN stays NaN
             const float inv = 1.f / l;
             const int w0 = (warp & 3) * 32;
             __nv_bfloat16* out = O + (orow + w0) * D;
@@ -508,12 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 v;
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                  : "r"(stg + r * 128 + ((ch ^ (r & 7)) << 4)) : "memory");
-                    if (w0 + r < qt.rows) *reinterpret_cast<uint4*>(out + size_t(r) * D + c * 64 + ch * 8) = v;
+                    if (w0 + r < rows_out) *reinterpret_cast<uint4*>(out + size_t(r) * D + c * 64 + ch * 8) = v;
                 }
                 __syncwarp();
             }
             tc_fence_before();
-            if (live && lse) lse[orow + row] = seen ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            if (row < rows_out && lse) lse[orow + row] = seen ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
     }
 

@@ -16,7 +16,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 65536;
 
 moc_status make_args(moc::WinArgs& a, int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, int64_t left,
                      int64_t right, int64_t sinks, int causal, const int32_t* q_len, const int32_t* kv_len,
-                     float scale) {
+                     int fill, float scale) {
     if (B < 0 || Hq < 0 || Hk < 0 || Lq < 0 || Lk < 0) return MOC_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return MOC_ERR_INVALID_ARG;
     if ((Hk == 0) != (Hq == 0) || (Hk > 0 && Hq % Hk != 0)) return MOC_ERR_INVALID_ARG;
@@ -38,6 +38,7 @@ moc_status make_args(moc::WinArgs& a, int B, int Hq, int Hk, int64_t Lq, int64_t
     a.q_len = q_len;
     a.kv_len = kv_len;
     a.scale = scale;
+    a.fill = fill ? 1 : 0;
     return MOC_OK;
 }
 
@@ -45,10 +46,11 @@ moc_status make_args(moc::WinArgs& a, int B, int Hq, int Hk, int64_t Lq, int64_t
 
 extern "C" moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                            const void* K, const void* V, int64_t left, int64_t right, int64_t sinks,
-                                           int causal, const int32_t* q_len, const int32_t* kv_len,
+                                           int causal, const int32_t* q_len, const int32_t* kv_len, int fill_rest,
                                            float softmax_scale, void* O, float* lse, moc_stream_t stream) {
     moc::WinArgs a{};
-    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len, softmax_scale);
+    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len, fill_rest,
+                                    softmax_scale);
     if (st != MOC_OK) return st;
     if (B == 0 || Hq == 0 || Lq == 0) return MOC_OK;
     if (!aligned16(Q) || !aligned16(O) || (Lk > 0 && (!aligned16(K) || !aligned16(V))) || !aligned4(lse))
@@ -67,18 +69,19 @@ extern "C" moc_status moc_window_device_error(int32_t* detail, moc_stream_t stre
 extern "C" size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d,
                                                            int64_t left, int64_t right, int64_t sinks, int causal) {
     moc::WinArgs a{};
-    if (make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, nullptr, nullptr, 1.f) != MOC_OK) return 0;
+    if (make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, nullptr, nullptr, 0, 1.f) != MOC_OK) return 0;
     return moc::plan_window_bwd(a, d).total;
 }
 
 extern "C" moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                                const void* K, const void* V, const void* O, const float* lse,
                                                const void* dO, int64_t left, int64_t right, int64_t sinks, int causal,
-                                               const int32_t* q_len, const int32_t* kv_len, float softmax_scale,
-                                               void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
+                                               const int32_t* q_len, const int32_t* kv_len, int fill_rest,
+                                               float softmax_scale, void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
                                                moc_stream_t stream) {
     moc::WinArgs a{};
-    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len, softmax_scale);
+    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len, fill_rest,
+                                    softmax_scale);
     if (st != MOC_OK) return st;
     if (B == 0 || Hq == 0 || (Lq == 0 && Lk == 0)) return MOC_OK;
     if (Lq > 0)

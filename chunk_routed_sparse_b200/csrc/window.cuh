@@ -26,6 +26,7 @@ struct WinArgs {
     const int32_t* q_len;       // [B] or null: Lq
     const int32_t* kv_len;      // [B] or null: Lk
     float scale;
+    int32_t fill;               // rows past the lengths: 0 left as they were, 1 written as empty
 };
 
 #ifdef __CUDACC__

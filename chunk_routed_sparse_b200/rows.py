@@ -171,7 +171,7 @@ def _rotary(rope, X, pos, transpose, out):
         raise ValueError("rope: expected a Rope")
     p, pb, pa = _positions(rope, pos, B, L, d, X.device)
     if out is None:
-        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        out = torch.empty_like(X, memory_format=torch.contiguous_format)
     else:
         _rows("out", out, X, X.shape)
     buf, at = _strides(X, out)
@@ -266,9 +266,9 @@ def qk_norm_rope_fwd(Q, K, V=None, wq=None, wk=None, rope: Optional[Rope] = None
     code = _weights(wq, wk, Q, d)
     p, pb, pa = _positions(rope, pos, B, L, d, Q.device)
     if out is None:
-        Qo = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-        Ko = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
-        Vo = torch.empty(V.shape, dtype=Q.dtype, device=Q.device) if V is not None else None
+        Qo = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        Ko = torch.empty_like(K, memory_format=torch.contiguous_format)
+        Vo = torch.empty_like(V, memory_format=torch.contiguous_format) if V is not None else None
     else:
         Qo, Ko, Vo = out
         _rows("out Q", Qo, Q, Q.shape)
@@ -299,9 +299,9 @@ def qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQo, dKo, dVo=None, out=None,
     code = _weights(wq, wk, Q, d)
     p, pb, pa = _positions(rope, pos, B, L, d, Q.device)
     if out is None:
-        dQ = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
-        dK = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
-        dV = torch.empty(K.shape, dtype=Q.dtype, device=Q.device) if dVo is not None else None
+        dQ = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        dK = torch.empty_like(K, memory_format=torch.contiguous_format)
+        dV = torch.empty_like(K, memory_format=torch.contiguous_format) if dVo is not None else None
     else:
         dQ, dK, dV = out
         _rows("out dQ", dQ, Q, Q.shape)
@@ -343,9 +343,7 @@ def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=No
     code = _weights(wq, wk, qkv, d)
     p, pb, pa = _positions(rope, pos, B, L, d, qkv.device)
     dt, dev = qkv.dtype, qkv.device
-    Q = torch.empty((B, Hq, L, d), dtype=dt, device=dev)
-    K = torch.empty((B, Hk, L, d), dtype=dt, device=dev)
-    V = torch.empty((B, Hk, L, d), dtype=dt, device=dev)
+    Q, K, V = qkv.new_empty((B, Hq, L, d)), qkv.new_empty((B, Hk, L, d)), qkv.new_empty((B, Hk, L, d))
     if not qkv.numel():
         return Q, K, V
     sb, sl, sh, _ = qkv.stride()
@@ -367,7 +365,7 @@ def qkv_norm_rope_bwd(qkv, Hq: int, Hk: int, wq, wk, rope, pos, eps, dQ, dK, dV,
     code = _weights(wq, wk, qkv, d)
     p, pb, pa = _positions(rope, pos, B, L, d, qkv.device)
     dev = qkv.device
-    dqkv = torch.empty(qkv.shape, dtype=qkv.dtype, device=dev)
+    dqkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
     dwq = torch.empty_like(wq) if want_dw and wq is not None else None
     dwk = torch.empty_like(wk) if want_dw and wk is not None else None
     ws = _bwd_workspace(dev, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None

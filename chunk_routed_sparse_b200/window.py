@@ -65,18 +65,19 @@ def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 
     B, Hq, Hk, Lq, Lk, d = _problem(Q, K, V, q_len, kv_len)
     left, right, sinks = _limits(left, right, sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
+    fill = O is None and lse is None
     if O is None:
-        O = torch.empty_like(Q) if q_len is None else torch.zeros_like(Q)
+        O = torch.empty_like(Q) if fill or q_len is None else torch.zeros_like(Q)
     else:
         _tensor("O", O, Q.shape, Q.device)
     if lse is None:
-        lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=Q.device)
-        if q_len is not None:
+        lse = Q.new_empty((B, Hq, Lq), dtype=torch.float32)
+        if not fill and q_len is not None:
             lse.fill_(-math.inf)
     else:
         _tensor("lse", lse, (B, Hq, Lq), Q.device, torch.float32)
     _call("moc_window_attention", Q.device, B, Hq, Hk, Lq, Lk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(), left, right,
-          sinks, 1 if causal else 0, _at(q_len), _at(kv_len), scale, O.data_ptr(), lse.data_ptr())
+          sinks, 1 if causal else 0, _at(q_len), _at(kv_len), fill, scale, O.data_ptr(), lse.data_ptr())
     return O, lse
 
 
@@ -96,9 +97,10 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
     for name, x, ref in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, K)):
         if x is not None:
             _tensor(name, x, ref.shape, Q.device)
-    dQ = (torch.empty_like(Q) if q_len is None else torch.zeros_like(Q)) if dQ is None else dQ
-    dK = (torch.empty_like(K) if kv_len is None else torch.zeros_like(K)) if dK is None else dK
-    dV = (torch.empty_like(K) if kv_len is None else torch.zeros_like(K)) if dV is None else dV
+    fill = dQ is None and dK is None and dV is None
+    dQ = (torch.empty_like(Q) if fill or q_len is None else torch.zeros_like(Q)) if dQ is None else dQ
+    dK = (torch.empty_like(K) if fill or kv_len is None else torch.zeros_like(K)) if dK is None else dK
+    dV = (torch.empty_like(K) if fill or kv_len is None else torch.zeros_like(K)) if dV is None else dV
     if ws is None:
         n = _on(Q.device, lib().moc_window_attention_bwd_workspace_bytes, B, Hq, Hk, Lq, Lk, d, left, right, sinks,
                 1 if causal else 0)
@@ -109,7 +111,7 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
         raise ValueError(f"ws: expected a contiguous tensor on {Q.device}")
     _call("moc_window_attention_bwd", Q.device, B, Hq, Hk, Lq, Lk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
           O.data_ptr(), lse.data_ptr(), dO.data_ptr(), left, right, sinks, 1 if causal else 0, _at(q_len), _at(kv_len),
-          scale, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+          fill, scale, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dQ, dK, dV
 
 

@@ -525,17 +525,18 @@ moc_status moc_qk_norm_rope_bwd(const moc_rope* rope, int dtype, int B, int Hq, 
  * left < 0 or right < 0: no limit on that side. O is the softmax of the scaled
  * scores over the visible keys applied to V, rounded once to bf16; lse (nullable)
  * fp32 [B][Hq][Lq] their log-sum-exp. A row that sees no key gets O = 0 and
- * lse = -inf. Rows t >= q_len[b] of O and lse are left as they were, and keys
- * that no row sees are not read into any result, whatever they hold. (A key
- * that only some rows of 256 see, and that holds an infinity or a NaN, can reach
- * the others as 0 x infinity.) softmax_scale > 0, finite. Lq, Lk < 2^28,
+ * lse = -inf. Rows t >= q_len[b] of O and lse are left as they were (fill_rest 0)
+ * or written as rows that see no key (1). Keys that no row sees are not read into
+ * any result, whatever they hold. (A key that only some rows of 256 see, and that
+ * holds an infinity or a NaN, can reach the others of them as 0 x infinity, and
+ * so is NaN there.) softmax_scale > 0, finite. Lq, Lk < 2^28,
  * B Hq Lq and B Hk Lk < 2^31 - 65536, B and Hq at most 65535. Asynchronous, no
  * workspace; a device-side wait that gives up is reported by
  * moc_window_device_error. */
 moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q, const void* K,
                                 const void* V, int64_t left, int64_t right, int64_t sinks, int causal,
-                                const int32_t* q_len, const int32_t* kv_len, float softmax_scale, void* O,
-                                float* lse, moc_stream_t stream);
+                                const int32_t* q_len, const int32_t* kv_len, int fill_rest, float softmax_scale,
+                                void* O, float* lse, moc_stream_t stream);
 
 /* Bytes of device workspace moc_window_attention_bwd needs on the current device
  * (0 on invalid arguments). */
@@ -550,13 +551,13 @@ size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t L
  * sums in fp32 (over the rows of every query head that reads the key head), each
  * result rounded once. Rows that see no key get dQ = 0, keys that no row sees
  * dK = dV = 0; rows of dQ past q_len and of dK, dV past kv_len are left as they
- * were. ws: 256-byte aligned, contents free before and after; two calls that may
+ * were (fill_rest 0) or set to 0 (1). ws: 256-byte aligned, contents free before and after; two calls that may
  * overlap need two. Deterministic on one device model. */
 moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                     const void* K, const void* V, const void* O, const float* lse, const void* dO,
                                     int64_t left, int64_t right, int64_t sinks, int causal, const int32_t* q_len,
-                                    const int32_t* kv_len, float softmax_scale, void* dQ, void* dK, void* dV,
-                                    void* ws, size_t ws_bytes, moc_stream_t stream);
+                                    const int32_t* kv_len, int fill_rest, float softmax_scale, void* dQ, void* dK,
+                                    void* dV, void* ws, size_t ws_bytes, moc_stream_t stream);
 
 /* Read and clear the current device's error word of the window calls, as
  * moc_check_device_error does for a workspace. Synchronises the stream. */

@@ -113,6 +113,8 @@ def test_forward_matches_the_definition(case):
     _check_fwd(O, lse, ref)
     O2, lse2 = moc.window_attention_fwd(Q, K, V, left, right, sinks, causal, ql, kl)
     assert torch.equal(O2, O) and torch.equal(lse2, lse)
+    lse2 = moc.window_attention_fwd(Q, K, V, left, right, sinks, causal, ql, kl, O=O2)[1]
+    assert torch.equal(O2, O) and torch.equal(lse2, lse)
     moc.check_window_error()
 
 
@@ -164,7 +166,7 @@ def test_large_scores_and_scale():
     assert (err <= 2 * U * 5 + 100 * math.exp(-7.8) * 0.13 * 10).all()
 
 
-def _check_bwd(got, ref, ql, kl, Lq, Lk):
+def _check_bwd(got, ref, ql, kl, Lq, Lk, rest=0):
     for name, size, k, lens, L in (("dQ", "sQ", 4 * U + 2 * WT, ql, Lq), ("dK", "sK", 4 * U + 2 * WT, kl, Lk),
                                    ("dV", "sV", U + WT, kl, Lk)):
         x, want = got[name].double(), ref[name]
@@ -177,7 +179,7 @@ def _check_bwd(got, ref, ql, kl, Lq, Lk):
                 rel = (err.square().sum() / want[b, :, :n].square().sum()).sqrt()
                 assert rel <= 2 * U, (name, b, float(rel))
             if lens is not None:
-                assert (x[b, :, n:] == 5).all(), name  # as they were
+                assert (x[b, :, n:] == rest).all(), name
 
 
 @pytest.mark.parametrize("case", CASES, ids=str)
@@ -192,7 +194,11 @@ def test_gradient_matches_the_definition(case):
     got = {n: torch.full_like(t, 5.0) for n, t in (("dQ", Q), ("dK", K), ("dV", V))}
     moc.window_attention_bwd(Q, K, V, O, lse, g, *args, **got)
     moc.check_window_error()
-    _check_bwd(got, ref, ql, kl, Lq, Lk)
+    _check_bwd(got, ref, ql, kl, Lq, Lk, rest=5)  # as they were
+    new = moc.window_attention_bwd(Q, K, V, O, lse, g, *args)
+    _check_bwd(dict(zip(("dQ", "dK", "dV"), new)), ref, ql, kl, Lq, Lk)
+    some = moc.window_attention_bwd(Q, K, V, O, lse, g, *args, dK=got["dK"])
+    assert torch.equal(some[0], new[0]) and torch.equal(some[2], new[2])
 
 
 def test_gradients_with_shared_first_keys_split_over_many_rows():

@@ -11,9 +11,9 @@ P = 4096  # never dereferenced: every call here is refused (or has nothing to do
 
 
 def _fwd(B=1, Hq=4, Hk=2, Lq=8, Lk=8, d=64, Q=P, K=P, V=P, left=-1, right=-1, sinks=0, causal=1, ql=None, kl=None,
-         scale=0.125, O=P, lse=None):
-    return moc.lib().moc_window_attention(B, Hq, Hk, Lq, Lk, d, Q, K, V, left, right, sinks, causal, ql, kl, scale, O,
-                                          lse, None)
+         fill=0, scale=0.125, O=P, lse=None):
+    return moc.lib().moc_window_attention(B, Hq, Hk, Lq, Lk, d, Q, K, V, left, right, sinks, causal, ql, kl, fill,
+                                          scale, O, lse, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -40,7 +40,7 @@ def test_backward_refusals_and_workspace():
     assert size(Lq=30000, Lk=30000) > size(Lq=30000, Lk=30000, sinks=0) + 2 * 128 * 64 * 4
 
     def bwd(ws=P, nb=1 << 40, lse=P, dQ=P, dK=P, O=P, Lq=300):
-        return lib.moc_window_attention_bwd(1, 4, 2, Lq, 300, 64, P, P, P, O, lse, P, 50, 0, 9, 1, None, None, 0.125, dQ,
+        return lib.moc_window_attention_bwd(1, 4, 2, Lq, 300, 64, P, P, P, O, lse, P, 50, 0, 9, 1, None, None, 0, 0.125, dQ,
                                             dK, P, ws, nb, None)
 
     assert bwd(ws=None) == 1 and bwd(ws=P + 16) == 1 and bwd(nb=n - 1) == 3
