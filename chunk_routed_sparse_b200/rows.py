@@ -86,12 +86,14 @@ class Rope:
             pass
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+# (absent in a build of torch without CUDA; only CUDA tensors get here)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle, no Stream object
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device: torch.device, fn, *args):
     """fn(*args) with the device current."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -99,12 +101,12 @@ def _on(device: torch.device, fn, *args):
 
 def _call(where: str, device: torch.device, *args):
     """Call lib().<where>(*args, stream) on the device and its current stream."""
-    i = device.index
-    if i == torch.cuda.current_device():
-        status = getattr(lib(), where)(*args, _raw_stream(i))
+    i, fn = device.index, getattr(lib(), where)
+    if i == _current_device():
+        status = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(i):
-            status = getattr(lib(), where)(*args, _raw_stream(i))
+            status = fn(*args, _raw_stream(i))
     if status != 0:
         raise MocError(status, where)
 
@@ -132,7 +134,7 @@ def _positions(rope: Optional[Rope], pos: Optional[torch.Tensor], B: int, L: int
         if pos is not None:
             raise ValueError("positions without a rotation")
         return None, 0, 0
-    if not isinstance(rope, Rope) or not rope.handle.value:
+    if not isinstance(rope, Rope) or not rope._h.value:
         raise ValueError("rope: expected an open Rope")
     if rope.dim > d:
         raise ValueError(f"the rotation covers {rope.dim} dims, heads have {d}")
@@ -152,16 +154,25 @@ def _positions(rope: Optional[Rope], pos: Optional[torch.Tensor], B: int, L: int
     return pos, pos.stride(0) if pos.dim() == 3 else 0, pos.stride(-2) if pos.dim() > 1 else 0
 
 
-_STRIDES = {n: ctypes.c_int64 * (3 * n) for n in (2, 6, 8)}
+_stride_arrays: dict = {}  # strides -> their host array and its address (read during a call only)
+
+
+def _stride_array(*vals):
+    hit = _stride_arrays.get(vals)
+    if hit is None:
+        if len(_stride_arrays) >= 512:
+            _stride_arrays.clear()
+        buf = (ctypes.c_int64 * len(vals))(*vals)
+        hit = _stride_arrays[vals] = (buf, ctypes.addressof(buf))
+    return hit
 
 
 def _strides(*tensors):
     """Batch, head and token strides of every tensor in one host array, and its address."""
-    vals = []
+    vals = ()
     for t in tensors:
         vals += t.stride()[:3] if t is not None else (0, 0, 0)
-    buf = _STRIDES[len(tensors)](*vals)
-    return buf, ctypes.addressof(buf)
+    return _stride_array(*vals)
 
 
 def _rotary(rope, X, pos, transpose, out):
@@ -347,8 +358,8 @@ def qkv_norm_rope_fwd(qkv, Hq: int, Hk: int, wq=None, wk=None, rope=None, pos=No
     if not qkv.numel():
         return Q, K, V
     sb, sl, sh, _ = qkv.stride()
-    buf = _STRIDES[6](sb, sh, sl, sb, sh, sl, sb, sh, sl, Hq * L * d, L * d, d, Hk * L * d, L * d, d, Hk * L * d, L * d, d)
-    at = ctypes.addressof(buf)
+    buf, at = _stride_array(sb, sh, sl, sb, sh, sl, sb, sh, sl, Hq * L * d, L * d, d, Hk * L * d, L * d, d, Hk * L * d,
+                            L * d, d)
     x, step = qkv.data_ptr(), sh * qkv.element_size()
     _call("moc_qk_norm_rope", dev, rope.handle if rope is not None else None, _DTYPE[dt], B, Hq, Hk, L, d, x, at,
           x + Hq * step, at + 24, x + (Hq + Hk) * step, at + 48, _at(wq), _at(wk), code, eps, _at(p), pb, pa,
@@ -372,9 +383,9 @@ def qkv_norm_rope_bwd(qkv, Hq: int, Hk: int, wq, wk, rope, pos, eps, dQ, dK, dV,
     sb, sl, sh, _ = qkv.stride()
     heads = Hq + 2 * Hk
     ob, ol = L * heads * d, heads * d
-    buf = _STRIDES[8](sb, sh, sl, sb, sh, sl, *dQ.stride()[:3], *dK.stride()[:3], *dV.stride()[:3], ob, d, ol, ob, d, ol,
-                      ob, d, ol)
-    at, x, y, eb = ctypes.addressof(buf), qkv.data_ptr(), dqkv.data_ptr(), qkv.element_size()
+    buf, at = _stride_array(sb, sh, sl, sb, sh, sl, *dQ.stride()[:3], *dK.stride()[:3], *dV.stride()[:3], ob, d, ol, ob,
+                            d, ol, ob, d, ol)
+    x, y, eb = qkv.data_ptr(), dqkv.data_ptr(), qkv.element_size()
     if not qkv.numel():  # no rows: addresses mean nothing, the weights' gradients are zero
         return dqkv, *(None if w is None else w.zero_() for w in (dwq, dwk))
     _call("moc_qk_norm_rope_bwd", dev, rope.handle if rope is not None else None, _DTYPE[qkv.dtype], B, Hq, Hk, L, d,
