@@ -16,6 +16,10 @@
 // launch. No atomics on results: they do not depend on the order of the units, which
 // are handed out longest first by a counter.
 //
+// Training step of the single-shot clip (causal over 6,239 keys and 512 first ones): dQ
+// 1.6 ms and dK / dV 2.0 ms, 1.16 and 1.25 PFLOP/s of executed products (6 d and 8 d a
+// pair), at the 1 kW power cap.
+//
 // D from the rounded O is off by what O's rounding carries, which a row of few keys
 // feels as much as the roundings of p and ds. As sum_u ds_tu = 0 for the exact D, the
 // dQ kernel adds the sum r of its unrounded ds to D for the dK / dV kernel, and walks

@@ -12,6 +12,9 @@
 //          MMAs (mma.sync; 16 rows fill its M, a 128-row tcgen05 tile would be an
 //          eighth used at best, and the bytes bound this kernel either way), running
 //          maximum and sum per warp in fp32; joined over the warps at the end.
+// One token of eight streams, 24 heads, 8,255 visible keys each (811 MB): 126 us, the
+// measured copy bandwidth. A fourth stage (one CTA an SM) takes 202 us; clusters of 1,
+// 2, 4 and 8 CTAs 131, 153, 129 and 144 us.
 // Rounding and masking as in the many-row kernel: P to bf16 before P V, sums of the
 // unrounded weights, keys past a run of visible ones never reach a product.
 #include "common.cuh"
@@ -327,8 +330,8 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // Split the keys over a cluster until four CTAs an SM are reached, while every CTA
-    // keeps two tiles.
+    // Split the keys over a cluster until there are four CTAs an SM (two are resident;
+    // the others even out streams of unlike lengths), while every CTA keeps two tiles.
     const int64_t heads = int64_t(a.B) * a.Hk;
     const int64_t keys = a.left == kWinOpen || a.right == kWinOpen
                              ? a.Lk

@@ -12,10 +12,15 @@
 //   warp 9 (one lane): S_q = Q K^T and O_q += P V (P from TMEM), alternating A and
 //          B; an item's last PV and the next item's first S are issued back to back.
 //   warps 0-3 / 4-7: softmax of tile A / B, one thread a row, running max and sum
-//          in fp32, P written over S as bf16 in two halves, so that the first half of
-//          P V runs under the second half's exponentials (a rounding of 2^-9 of each weight; the
-//          sum is of the unrounded weights); the epilogue stages O through shared
-//          memory into whole 128-byte row pieces.
+//          in fp32, P written over S as bf16 (2^-8 of each weight at most; the sum is of
+//          the unrounded weights) in two halves, so that the first half of P V runs
+//          under the second half's exponentials (5 %); the epilogue stages O through
+//          shared memory into whole 128-byte row pieces.
+// Single-shot clip (12 heads, 33,272 tokens, d = 128, 512 first keys and 1,560 on either
+// side; 722 GFLOP on visible pairs): 0.66 ms in short runs (1.10 PFLOP/s), 0.77 ms
+// once the 1 kW power cap holds the clock. Between tensor core (57 % busy) and
+// exponentials (58 %) each tile's chain of product, softmax and product sets the pace;
+// a share of the exponentials on the FMA pipe measured slower.
 // A tile that one of A, B cannot see is skipped for it; a tile that every row of a
 // warp sees whole takes no masking. Keys past a tile's end are other rows' or none:
 // their scores become -inf and their V rows are zeroed in shared memory (0 x NaN).
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!__all_sync(0xffffffffu, !live || ns >= 128 || (lo <= 0 && hi >= 128))) {
                     // masked in TMEM, 64 columns at a time, before the scores are loaded: masking
                     // them among the 128 loaded registers spilled in every tile (1.09 ms against
-                    // 0.71 ms on the single-shot clip)
+                    // 0.70 ms on the single-shot clip)
 #pragma unroll 1
                     for (int w = 0; w < 128; w += 64) {
                         const uint32_t k0 = win::bits(0, ns - w) | win::bits(lo - w, hi - w);

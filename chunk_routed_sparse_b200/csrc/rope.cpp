@@ -100,8 +100,10 @@ extern "C" moc_status moc_build_rope(const moc_rope_desc* d, moc_rope** out) {
         const int n = d->axis_dim[a];
         long double theta = d->theta;
         if (d->scaling == MOC_ROPE_NTK && n > 2) theta *= powl(s, (long double)n / (n - 2));
-        for (int j = 0; j < n / 2; ++j, ++i) {
-            long double w = powl(theta, -2.0L * j / n);
+        const long double ratio = powl(theta, -2.0L / n);
+        long double plain = 1.0L;  // theta^(-2 j / n): 63 products in 64 bits lose nothing that fp64 shows
+        for (int j = 0; j < n / 2; ++j, ++i, plain *= ratio) {
+            long double w = plain;
             if (d->scaling == MOC_ROPE_LINEAR) w /= s;
             if (d->scaling == MOC_ROPE_YARN) {
                 const long double turns = (long double)d->original_length * w / two_pi;
