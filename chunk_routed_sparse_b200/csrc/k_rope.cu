@@ -33,6 +33,7 @@ namespace moc {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kBwdCtas = 5;  // resident CTAs of the backward kernel an SM
 constexpr int kRows = 4;  // rows of one lane group in flight
 
 // ---- eight elements of a row -------------------------------------------------
@@ -321,42 +322,52 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
 // A persistent CTA strides over token tiles, one tensor after the other (one
 // weight's partial gradient in registers at a time); the parts of a CTA are added
 // through shared memory in thread order and those of all CTAs by rows_dw_kernel in
-// CTA order: no atomics. Four rows of each tensor in flight a lane group, four CTAs
-// an SM: 160 us on the single-shot step (126 us of bytes at the measured copy rate)
-// against 165 us with two rows and five CTAs.
+// CTA order: no atomics. Rows come in steps of two, copied by cp.async into slots of
+// shared memory that belong to the thread that reads them (no barrier), up to three
+// steps ahead: loads into registers leave 16 warps an SM idle between their rounds
+// (163 us on the single-shot step against 138 us; its bytes take 126 us at the
+// measured copy rate). Rows off 16-byte boundaries are loaded when they are used.
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
 template <typename T, int D, bool HALF, bool AL>
-__global__ void __launch_bounds__(kThreads, 4) rows_bwd_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int LPR = D / 8, TPC = kThreads / LPR, ROWS = sizeof(T) == 4 ? 2 : 4;
+__global__ void __launch_bounds__(kThreads, kBwdCtas) rows_bwd_kernel(const __grid_constant__ RowArgs a) {
+    constexpr int LPR = D / 8, TPC = kThreads / LPR, RS = 2;
+    constexpr int W = sizeof(T) / 2;              // 16-byte words of a lane's eight elements
+    constexpr int ST = sizeof(T) == 4 ? 2 : 4;    // steps in the ring
     __shared__ uint64_t turn[kMaxRopePairs];
     __shared__ uint8_t axis[kMaxRopePairs];
     __shared__ __align__(16) float ws[D];
     __shared__ float red[TPC][D];
+    __shared__ __align__(16) uint4 ring[AL ? ST * RS * 2 * W * kThreads : 1];
     tab_to_smem(a, turn, axis);
     const int r = threadIdx.x % LPR, e0 = 8 * r;
     const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
+    const int64_t step = int64_t(gridDim.x) * TPC, first = int64_t(blockIdx.x) * TPC;
+    // slot of (stage, row of the step, tensor): word w of this thread
+    const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
+    auto slot = [&](int st, int u, int x) { return slot0 + uint32_t(((st * RS + u) * 2 + x) * W) * (kThreads * 16); };
+    auto at = [&](const int64_t (&st)[3], int64_t t0) -> int64_t {  // a tile's token of this lane group
+        const int64_t tok = t0 + threadIdx.x / LPR;
+        const int t = tok < a.tokens ? int(tok) : a.tokens - 1;
+        const int b = t / a.L;
+        return b * st[0] + (t - b * a.L) * st[2] + e0;
+    };
     int base = 0;
 #pragma unroll 1
     for (int k = 0; k < 3; ++k) {
         const RowSec& sec = a.sec[k];
         const int lo = max(h_lo - base, 0), hi = min(h_hi - base, sec.H);
         base += sec.H;
-        if (k < 2) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < D; i += kThreads) ws[i] = weight<T>(sec.w, a.w_fp32, i);
-            __syncthreads();
-        }
-        float dw[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+        if (k == 2) {  // values: the gradient only changes its layout
 #pragma unroll 1
-        for (int64_t t0 = int64_t(blockIdx.x) * TPC; lo < hi && t0 < a.tokens; t0 += int64_t(gridDim.x) * TPC) {
-            const int64_t tok = t0 + threadIdx.x / LPR;
-            const bool live = tok < a.tokens;
-            const int t = live ? int(tok) : a.tokens - 1;
-            const int b = t / a.L, l = t - b * a.L;
-            const T* g = static_cast<const T*>(sec.g) + b * sec.gs[0] + l * sec.gs[2] + e0;
-            T* y = static_cast<T*>(sec.y) + b * sec.ys[0] + l * sec.ys[2] + e0;
-            if (k == 2) {  // values: the gradient only changes its layout
+            for (int64_t t0 = first; lo < hi && t0 < a.tokens; t0 += step) {
+                const T* g = static_cast<const T*>(sec.g) + at(sec.gs, t0);
+                T* y = static_cast<T*>(sec.y) + at(sec.ys, t0);
+                const bool live = t0 + threadIdx.x / LPR < a.tokens;
 #pragma unroll 1
                 for (int h = lo; h < hi; h += kRows) {
                     Raw<T> raw[kRows];
@@ -367,23 +378,89 @@ __global__ void __launch_bounds__(kThreads, 4) rows_bwd_kernel(const __grid_cons
                     for (int u = 0; u < kRows; ++u)
                         if (h + u < hi && live) store_raw<T, AL>(y + (h + u) * sec.ys[1], raw[u]);
                 }
-                continue;
             }
-            const T* x = static_cast<const T*>(sec.x) + b * sec.xs[0] + l * sec.xs[2] + e0;
+            continue;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < D; i += kThreads) ws[i] = weight<T>(sec.w, a.w_fp32, i);
+        __syncthreads();
+        float dw[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+        // the next step to request: tile pt, head ph
+        int64_t pt = first;
+        int ph = lo, pst = 0;
+        const T *px = nullptr, *pg = nullptr;
+        auto rows_at = [&](int64_t t0) {
+            px = static_cast<const T*>(sec.x) + at(sec.xs, t0);
+            pg = static_cast<const T*>(sec.g) + at(sec.gs, t0);
+        };
+        auto request = [&]() {
+            if constexpr (AL) {
+                if (pt < a.tokens) {
+#pragma unroll
+                    for (int u = 0; u < RS; ++u) {
+                        if (ph + u >= hi) break;
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            cp_async16(slot(pst, u, 0) + w * (kThreads * 16), reinterpret_cast<const uint4*>(px + (ph + u) * sec.xs[1]) + w, 16);
+                            cp_async16(slot(pst, u, 1) + w * (kThreads * 16), reinterpret_cast<const uint4*>(pg + (ph + u) * sec.gs[1]) + w, 16);
+                        }
+                    }
+                    ph += RS;
+                    if (ph >= hi) {
+                        ph = lo;
+                        pt += step;
+                        if (pt < a.tokens) rows_at(pt);
+                    }
+                }
+                cp_async_commit();
+                pst = pst + 1 == ST ? 0 : pst + 1;
+            }
+        };
+        if (lo < hi) {
+            if (first < a.tokens) rows_at(first);
+#pragma unroll
+            for (int i = 0; i < ST - 1; ++i) request();
+        }
+        int st = 0;
+#pragma unroll 1
+        for (int64_t t0 = first; lo < hi && t0 < a.tokens; t0 += step) {
+            const int64_t tok = t0 + threadIdx.x / LPR;
+            const bool live = tok < a.tokens;
+            const int t = live ? int(tok) : a.tokens - 1;
+            const int b = t / a.L, l = t - b * a.L;
+            T* y = static_cast<T*>(sec.y) + b * sec.ys[0] + l * sec.ys[2] + e0;
+            if (!AL) rows_at(t0);
             Trig<HALF> tr;
             trig<HALF>(a, turn, axis, b, l, e0, tr);
 #pragma unroll 1
-            for (int h = lo; h < hi; h += ROWS) {
-                Raw<T> rx[ROWS], rg[ROWS];
+            for (int h = lo; h < hi; h += RS) {
+                Raw<T> rx[RS], rg[RS];
+                if constexpr (AL) {
+                    request();
+                    cp_async_wait<ST - 1>();
 #pragma unroll
-                for (int u = 0; u < ROWS; ++u) {
-                    if (h + u < hi) {
-                        load_raw<T, AL>(x + (h + u) * sec.xs[1], rx[u]);
-                        load_raw<T, AL>(g + (h + u) * sec.gs[1], rg[u]);
+                    for (int u = 0; u < RS; ++u) {
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            const uint4 vx = lds16(slot(st, u, 0) + w * (kThreads * 16)), vg = lds16(slot(st, u, 1) + w * (kThreads * 16));
+                            rx[u].w[4 * w] = vx.x, rx[u].w[4 * w + 1] = vx.y, rx[u].w[4 * w + 2] = vx.z, rx[u].w[4 * w + 3] = vx.w;
+                            rg[u].w[4 * w] = vg.x, rg[u].w[4 * w + 1] = vg.y, rg[u].w[4 * w + 2] = vg.z, rg[u].w[4 * w + 3] = vg.w;
+                        }
+                    }
+                    st = st + 1 == ST ? 0 : st + 1;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < RS; ++u) {
+                        if (h + u < hi) {
+                            load_raw<T, AL>(px + (h + u) * sec.xs[1], rx[u]);
+                            load_raw<T, AL>(pg + (h + u) * sec.gs[1], rg[u]);
+                        }
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < ROWS; ++u) {
+                for (int u = 0; u < RS; ++u) {
                     if (h + u >= hi) break;
                     float v[8], q[8], w[8];
                     unpack<T>(rx[u], v);
@@ -407,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_bwd_kernel(const __grid_cons
                 }
             }
         }
-        if (k == 2 || a.part == nullptr) continue;
+        if constexpr (AL) cp_async_wait<0>();
+        if (a.part == nullptr) continue;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < 8; ++j) red[threadIdx.x / LPR][e0 + j] = dw[j];
@@ -483,7 +561,7 @@ static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t most, int* heads
 }
 
 static dim3 rows_bwd_grid(int d, int64_t tokens, int heads, int* heads_per_cta) {
-    return rows_grid(d, tokens, heads, 4 * int64_t(sm_count()), heads_per_cta);  // four CTAs an SM are resident
+    return rows_grid(d, tokens, heads, kBwdCtas * int64_t(sm_count()), heads_per_cta);
 }
 
 cudaError_t launch_rows_fwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
