@@ -40,10 +40,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kProbeKeys = 384;
 
-// Row statistics (log2 sum exp2 of the scores, D), rows of a head padded to an even
-// count (16-byte copies of any even row) and 128 more at the end: +inf, 0 where there
-// is no row or the row sees no key, so that every p of it is zero.
-__device__ __forceinline__ int64_t stat_row(const WinArgs& a, int64_t head) { return head * ((a.Lq + 1) & ~1); }
+// Row statistics, negated for the sums they enter: - log2 sum exp2 of the scores and
+// - D, rows of a head padded to a multiple of four (16-byte copies from any fourth row)
+// and 128 more at the end; -inf and 0 where there is no row or the row sees no key, so
+// that every p of it is zero.
+__host__ __device__ __forceinline__ int64_t stat_rows(int Lq) { return (int64_t(Lq) + 3) & ~int64_t(3); }
 
 struct Shared {
     int item[2];
@@ -68,18 +69,18 @@ template <int D>
 __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant__ WinArgs a,
                                                            const __nv_bfloat16* __restrict__ O,
                                                            const __nv_bfloat16* __restrict__ dO,
-                                                           const float* __restrict__ lse, float2* __restrict__ stats,
-                                                           int32_t* __restrict__ work) {
+                                                           const float* __restrict__ lse, float* __restrict__ nl2,
+                                                           float* __restrict__ nd, int32_t* __restrict__ work) {
     constexpr int LPR = D / 8, RPC = 256 / LPR;  // lanes a row (16 bytes each), rows a step
     if (blockIdx.x == 0 && threadIdx.x < 2) work[threadIdx.x] = 0;
-    const int per = (a.Lq + 1) & ~1;
+    const int per = int(stat_rows(a.Lq));
     const int64_t heads = int64_t(a.B) * a.Hq, total = heads * per + 128;
     const int r = threadIdx.x % LPR;
     for (int64_t i0 = int64_t(blockIdx.x) * RPC; i0 < total; i0 += int64_t(gridDim.x) * RPC) {
         const int64_t i = i0 + threadIdx.x / LPR;
         const int64_t head = per > 0 ? i / per : heads;
         const int t = int(i - head * per);
-        float acc = 0.f, l2 = INFINITY;
+        float acc = 0.f, l2 = -INFINITY;
         if (head < heads && t < win::seq(a, int(head / a.Hq)).m) {
             const size_t row = size_t(head) * a.Lq + t;
             const uint4 x = ldg_nc16(O + row * D + r * 8), y = ldg_nc16(dO + row * D + r * 8);
@@ -90,11 +91,14 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
                 acc = fmaf(bf16hi(xs[k]), bf16hi(ys[k]), acc);
             }
             const float v = __ldg(lse + row);
-            if (v > -INFINITY || v != v) l2 = v * kLog2e;
+            if (v > -INFINITY || v != v) l2 = -v * kLog2e;
         }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o, LPR);
-        if (r == 0 && i < total) stats[i] = make_float2(l2, l2 == INFINITY ? 0.f : acc);
+        if (r == 0 && i < total) {
+            nl2[i] = l2;
+            nd[i] = l2 == -INFINITY ? 0.f : -acc;
+        }
     }
 }
 
@@ -168,8 +172,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ WinArgs a, int n_units, int nqt, float2* __restrict__ stats,
-                     int32_t* __restrict__ work, int32_t* __restrict__ hdr,
+                     const __grid_constant__ WinArgs a, int n_units, int nqt, const float* __restrict__ nl2,
+                     float* __restrict__ nd, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
                      __nv_bfloat16* __restrict__ dQ) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -355,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wg = warp >> 2, row = tid & 127;
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
         const float sl2 = a.scale * kLog2e;
+        const uint64_t sc2 = f2_pack(sl2, sl2);
         uint32_t gt = 0, nu = 0, ns[2] = {0, 0}, gk = 0, nx = 0;
         for (int it = 0;; ++it) {
             const int slot = it & 1;
@@ -368,11 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rows_out <= 0) continue;
             const bool live = row < x.rows;
             const size_t rowg = (size_t(x.b) * a.Hq + x.hq) * size_t(a.Lq) + size_t(x.t0) + row;
-            float2* my = stats + stat_row(a, int64_t(x.b) * a.Hq + x.hq) + x.t0 + row;
-            const float2 st = live ? *my : make_float2(INFINITY, 0.f);
-            const float lse2 = st.x;
-            float drow = st.y;
-            // adds to drow what the two warpgroups have for their halves of the row's keys;
+            const int64_t srow = (int64_t(x.b) * a.Hq + x.hq) * stat_rows(a.Lq) + x.t0 + row;
+            const float l2 = live ? nl2[srow] : -INFINITY;
+            float drow = live ? nd[srow] : 0.f;  // - D
+            // takes from drow what the two warpgroups have for their halves of the row's keys;
             // exchanges alternate between two buffers, so that one's values are read before
             // the next but one overwrites them
             auto add_both = [&](float v) -> bool {
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(B_SUM));
                 if (!wait_bar_warp(bar(B_SUM), nx & 1, abort, hdr, 255)) return false;
                 ++nx;
-                drow += sums[row] + sums[128 + row];
+                drow -= sums[row] + sums[128 + row];
                 return true;
             };
             uint64_t ra = 0, rb = 0;  // packed sums of the unrounded ds
@@ -418,7 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
                 tmem_wait_ld_regs(s);
 #pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c]), sl2, -lse2)));
+                for (int c = 0; c < 32; ++c) {
+                    float p0, p1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, f2_pack(l2, l2)), p0, p1);
+                    s[2 * c] = __float_as_uint(ex2(p0));
+                    s[2 * c + 1] = __float_as_uint(ex2(p1));
+                }
                 if (!wait_bar_warp(bar(B_DP_FULL), gt & 1, abort, hdr, 253)) { stop = true; break; }
                 tc_fence_after();
                 if (masked) {  // dP of a key past the lengths may be NaN
@@ -428,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
                 uint32_t p[64], pk[32];
+                const uint64_t nd2 = f2_pack(drow, drow);
                 tmem_ld32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
                 tmem_ld32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
                 tmem_wait_ld_regs(p);
@@ -435,10 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(B_DP_READ));
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float d0 = __uint_as_float(s[2 * c]) * (__uint_as_float(p[2 * c]) - drow);
-                    const float d1 = __uint_as_float(s[2 * c + 1]) * (__uint_as_float(p[2 * c + 1]) - drow);
-                    if (c & 1) rb = f2_add(rb, f2_pack(d0, d1));
-                    else ra = f2_add(ra, f2_pack(d0, d1));
+                    const uint64_t d = f2_mul(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])),
+                                              f2_add(f2_pack(__uint_as_float(p[2 * c]), __uint_as_float(p[2 * c + 1])), nd2));
+                    if (c & 1) rb = f2_add(rb, d);
+                    else ra = f2_add(ra, d);
+                    float d0, d1;
+                    f2_unpack(d, d0, d1);
                     pk[c] = pack_bf16(d0, d1);
                 }
                 tmem_st32(s_addr, pk);
@@ -463,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // dq_t = scale * accumulator; this warpgroup's half of the columns
             if (x.tiles > 0) {
                 if (!add_both(half_sum())) break;
-                if (wg == 0 && live && lse2 < INFINITY) *my = make_float2(lse2, drow);
+                if (wg == 0 && live && l2 != -INFINITY) nd[srow] = drow;
                 if (!wait_bar_warp(bar(B_DQ_DONE), nu & 1, abort, hdr, 254)) break;
                 ++nu;
                 tc_fence_after();
@@ -514,6 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of a tile in a row, then its math: 2.80 ms on the single-shot training step against
 // 1.97 ms; two TMEM buffers of 64 rows each: 3.14 ms, a 64-column product takes as
 // long as a 128-column one.)
+// At d = 64 the accumulators leave room for a second S^T: it runs a tile ahead (the
+// odd padded batch: 43.6 against 45.1 us).
 //   warp 8 (one lane): units and TMA: K and V of a unit, Q tiles into a 3-stage ring,
 //          dO tiles and row statistics into a 2-stage ring.
 //   warp 9 (one lane): the products.
@@ -524,7 +538,6 @@ namespace dkv {
 constexpr int kThreads = 384;
 // launched at 168 registers a thread: 2 x 128 x 216 + 128 x 72 = 384 x 168
 constexpr int kRegsCompute = 216, kRegsOther = 72;
-constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 384;
 
 template <int D>
 struct Cfg {
@@ -532,26 +545,32 @@ struct Cfg {
     static constexpr int kSlabBytes = 128 * 128;
     static constexpr int kTileBytes = kSlabs * kSlabBytes;
     static constexpr int kQStages = 3, kOStages = 2;
-    static constexpr int kStatBytes = kTile * 8;
+    static constexpr int kStatBytes = kTile * 8;  // 128 of either statistic
     static constexpr int oK = 0;
     static constexpr int oV = oK + kTileBytes;
     static constexpr int oQ = oV + kTileBytes;
     static constexpr int oDO = oQ + kQStages * kTileBytes;
-    static constexpr int oStat = oDO + kOStages * kTileBytes;  // [stage][row] (log-sum-exp, D)
+    static constexpr int oStat = oDO + kOStages * kTileBytes;  // [stage][- log-sum-exp | - D][row]
     static constexpr int oBar = oStat + kOStages * kStatBytes;
     // the dynamic shared memory of a kernel without static shared memory starts on a
     // 1024-byte boundary (checked at the start): no room for slack at d = 128
     static constexpr int kSmem = oBar + 256 > 120 * 1024 ? oBar + 256 : 120 * 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
+    // TMEM columns. d = 64 leaves room for a second S^T.
+    static constexpr bool kTwoS = D == 64;
+    static constexpr uint32_t kColDPT = kTwoS ? 256 : 128, kColDV = kTwoS ? 384 : 256, kColDK = kTwoS ? 448 : 384;
+    static __device__ __forceinline__ uint32_t col_st(uint32_t g) { return kTwoS && (g & 1) ? 128u : 0u; }
     static constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0);
     static constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, 1);
 };
 
 enum {
     B_ITEM_FULL = 0, B_ITEM_EMPTY = 2, B_KV_FULL = 4, B_KV_EMPTY = 5, B_Q_FULL = 6, B_Q_EMPTY = 9, B_O_FULL = 12,
-    B_O_EMPTY = 14, B_S_FULL = 16, B_P_FULL = 17, B_DP_FULL = 18, B_DS_FULL = 19, B_ACC_DONE = 20, B_EPI_DONE = 21,
-    B_MMA_DONE = 22, B_TAIL = 23, B_P_HALF = 25, B_COUNT = 26
+    B_O_EMPTY = 14, B_S_FULL = 16, B_P_FULL = 18, B_P_HALF = 20, B_DP_FULL = 22, B_DS_FULL = 23, B_ACC_DONE = 24,
+    B_EPI_DONE = 25, B_MMA_DONE = 26, B_TAIL = 27, B_COUNT = 29
 };
+// S_FULL, P_HALF and P_FULL: one for even tiles and one for odd. With two S^T a
+// warpgroup may be a tile ahead of the other, and must not complete its phase.
 static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 
 // A unit: a key tile of a (batch, key head), all of its row tiles or one split of them.
@@ -588,7 +607,7 @@ __device__ __forceinline__ void decode(const WinArgs& a, const WinBwdPlan& p, in
     int p_lo = first ? -(1 << 30) : x.k0 - a.right;
     if (a.causal) p_lo = max(p_lo, x.k0);
     const int p_hi = first ? (1 << 30) : x.k0 + x.nk - 1 + a.left;  // last position
-    x.t_lo = max(p_lo - x.seq.shift, 0) & ~1;                       // even: 16-byte copies of the statistics
+    x.t_lo = max(p_lo - x.seq.shift, 0) & ~3;                       // 16-byte copies of the statistics
     x.t_hi = min(p_hi - x.seq.shift + 1, x.seq.m);
     if (x.t_hi <= x.t_lo) return;
     x.per_head = (x.t_hi - x.t_lo + kTile - 1) / kTile;
@@ -597,13 +616,25 @@ __device__ __forceinline__ void decode(const WinArgs& a, const WinBwdPlan& p, in
     x.i0 = int(int64_t(total) * split / splits);
     x.i1 = int(int64_t(total) * (split + 1) / splits);
 }
-// Row tile i of a unit: query head, first row, rows.
-__device__ __forceinline__ void row_tile(const WinArgs& a, const Unit& x, int i, int& hq, int& t0, int& n) {
-    const int g = i / x.per_head;
-    hq = x.hk * a.group + g;
-    t0 = x.t_lo + (i - g * x.per_head) * kTile;
-    n = min(kTile, x.t_hi - t0);
-}
+// Walk over a unit's row tiles, the heads of the group one after the other.
+struct RowWalk {
+    int r, hq, t0;  // tile of the head, query head, first row
+    __device__ __forceinline__ RowWalk(const WinArgs& a, const Unit& x) {
+        const int g = x.i0 / max(x.per_head, 1);
+        r = x.i0 - g * x.per_head;
+        hq = x.hk * a.group + g;
+        t0 = x.t_lo + r * kTile;
+    }
+    __device__ __forceinline__ int rows(const Unit& x) const { return min(kTile, x.t_hi - t0); }
+    __device__ __forceinline__ void next(const Unit& x) {
+        t0 += kTile;
+        if (++r == x.per_head) {
+            r = 0;
+            t0 = x.t_lo;
+            ++hq;
+        }
+    }
+};
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -616,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                       const __grid_constant__ WinArgs a, const __grid_constant__ WinBwdPlan p, int n_units,
-                      const float2* __restrict__ stats, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
+                      const float* __restrict__ nl2, const float* __restrict__ nd, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
                       float* __restrict__ parts, __nv_bfloat16* __restrict__ dK, __nv_bfloat16* __restrict__ dV) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -637,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 1;
             if (x == B_ITEM_EMPTY || x == B_ITEM_EMPTY + 1) n = 1 + 256;
             if (x == B_O_EMPTY || x == B_O_EMPTY + 1) n = 1 + 256;  // dV has read dO, the warps the statistics
-            if (x == B_P_FULL || x == B_P_HALF || x == B_DS_FULL || x == B_EPI_DONE) n = 256;
+            if ((x >= B_P_FULL && x < B_P_HALF + 2) || x == B_DS_FULL || x == B_EPI_DONE) n = 256;
             if (x == B_TAIL || x == B_TAIL + 1) n = 128;
             mbar_init(bar(x), n);
         }
@@ -682,11 +713,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(sK + s * C::kSlabBytes, &tmK, bar(B_KV_FULL), 64 * s, krow);
                     tma_load_2d(sV + s * C::kSlabBytes, &tmV, bar(B_KV_FULL), 64 * s, krow);
                 }
-                for (int i = x.i0; i < x.i1; ++i, ++g) {
-                    int hq, t0, n;
-                    row_tile(a, x, i, hq, t0, n);
-                    const int64_t head = int64_t(x.b) * a.Hq + hq;
-                    const int qrow = int(head * a.Lq) + t0;
+                RowWalk walk(a, x);
+                for (int i = x.i0; i < x.i1; ++i, ++g, walk.next(x)) {
+                    const int64_t head = int64_t(x.b) * a.Hq + walk.hq;
+                    const int qrow = int(head * a.Lq) + walk.t0;
                     const uint32_t qs = g % 3, os = g & 1;
                     if (!wait_bar(bar(B_Q_EMPTY + qs), ((g / 3) & 1) ^ 1, abort, hdr, 263)) { stop = true; break; }
                     mbar_expect_tx(bar(B_Q_FULL + qs), C::kTileBytes);
@@ -698,7 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int s = 0; s < C::kSlabs; ++s)
                         tma_load_2d(sDO + os * C::kTileBytes + s * C::kSlabBytes, &tmDO, bar(B_O_FULL + os), 64 * s, qrow);
-                    bulk_load(base + C::oStat + os * C::kStatBytes, stats + stat_row(a, head) + t0, C::kStatBytes,
+                    const int64_t srow = head * stat_rows(a.Lq) + walk.t0;
+                    bulk_load(base + C::oStat + os * C::kStatBytes, nl2 + srow, C::kStatBytes / 2, bar(B_O_FULL + os));
+                    bulk_load(base + C::oStat + os * C::kStatBytes + C::kStatBytes / 2, nd + srow, C::kStatBytes / 2,
                               bar(B_O_FULL + os));
                 }
             }
@@ -720,23 +752,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t gb = sDO + (t & 1) * C::kTileBytes;
                 const uint32_t acc = first ? 0u : 1u;
                 // the first 32 rows of either warpgroup, then the others
-                if (!wait_bar_warp(bar(B_P_HALF), t & 1, abort, hdr, 277)) return false;
+                if (!wait_bar_warp(bar(B_P_HALF + (t & 1)), (t >> 1) & 1, abort, hdr, 277)) return false;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         if ((kk & 2) == 0)
-                            umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
+                            umma_ts(tmem + C::kColDV, tmem + C::col_st(t) + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
                                     C::kIdescAcc, kk > 0 ? 1u : acc);
                 }
                 __syncwarp();
-                if (!wait_bar_warp(bar(B_P_FULL), t & 1, abort, hdr, 268)) return false;
+                if (!wait_bar_warp(bar(B_P_FULL + (t & 1)), (t >> 1) & 1, abort, hdr, 268)) return false;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         if ((kk & 2) != 0)
-                            umma_ts(tmem + kColDV, tmem + kColST + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
+                            umma_ts(tmem + C::kColDV, tmem + C::col_st(t) + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
                                     C::kIdescAcc, 1u);
                     umma_commit(bar(B_O_EMPTY + (t & 1)));
                 }
@@ -751,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t acc = first ? 0u : 1u;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(tmem + kColDK, tmem + kColDPT + pcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
+                        umma_ts(tmem + C::kColDK, tmem + C::kColDPT + pcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
                                 C::kIdescAcc, kk > 0 ? 1u : acc);
                     umma_commit(bar(B_Q_EMPTY + t % 3));
                 }
@@ -782,23 +814,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int i0 = uniform(x.i0), i1 = uniform(x.i1);
                 if (i0 >= i1) continue;
                 if (!wait_bar_warp(bar(B_KV_FULL), nu & 1, abort, hdr, 271)) break;
-                for (int i = i0; i < i1; ++i, ++g) {
-                    if (i == i0 + 1 && nu > 0 && !wait_bar_warp(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 272)) { stop = true; break; }
-                    if (i > i0 && !issue_dv(g - 1, i - 1 == i0)) { stop = true; break; }
-                    if (!wait_bar_warp(bar(B_Q_FULL + g % 3), (g / 3) & 1, abort, hdr, 273)) { stop = true; break; }
+                auto issue_s = [&](uint32_t t) -> bool {  // S^T of tile t
+                    if (!wait_bar_warp(bar(B_Q_FULL + t % 3), (t / 3) & 1, abort, hdr, 273)) return false;
                     tc_fence_after();
-                    issue_ss(kColST, sK, sQ + (g % 3) * C::kTileBytes, bar(B_S_FULL));
-                    if (i > i0 && !issue_dk(g - 1, i - 1 == i0)) { stop = true; break; }
-                    if (!wait_bar_warp(bar(B_O_FULL + (g & 1)), (g >> 1) & 1, abort, hdr, 274)) { stop = true; break; }
+                    issue_ss(C::col_st(t), sK, sQ + (t % 3) * C::kTileBytes, bar(B_S_FULL + (t & 1)));
+                    return true;
+                };
+                auto issue_dp = [&](uint32_t t) -> bool {  // dP^T of tile t
+                    if (!wait_bar_warp(bar(B_O_FULL + (t & 1)), (t >> 1) & 1, abort, hdr, 274)) return false;
                     tc_fence_after();
-                    issue_ss(kColDPT, sV, sDO + (g & 1) * C::kTileBytes, bar(B_DP_FULL));
+                    issue_ss(C::kColDPT, sV, sDO + (t & 1) * C::kTileBytes, bar(B_DP_FULL));
+                    return true;
+                };
+                // both warpgroups have read the previous unit's dV and dK
+                auto accumulators = [&]() -> bool {
+                    return nu == 0 || wait_bar_warp(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 272);
+                };
+                if constexpr (C::kTwoS) {
+                    // S^T a tile ahead: the exponentials never wait for it
+                    if (!issue_s(g)) break;
+                    for (int i = i0; i < i1; ++i, ++g) {
+                        if (!issue_dp(g) || (i + 1 < i1 && !issue_s(g + 1))) { stop = true; break; }
+                        if (i + 1 == i1 && leader) umma_commit(bar(B_KV_EMPTY));
+                        __syncwarp();
+                        if ((i == i0 && !accumulators()) || !issue_dv(g, i == i0) || !issue_dk(g, i == i0)) { stop = true; break; }
+                    }
+                    if (stop) break;
+                } else {
+                    for (int i = i0; i < i1; ++i, ++g) {
+                        if (i == i0 + 1 && !accumulators()) { stop = true; break; }
+                        if (i > i0 && !issue_dv(g - 1, i - 1 == i0)) { stop = true; break; }
+                        if (!issue_s(g)) { stop = true; break; }
+                        if (i > i0 && !issue_dk(g - 1, i - 1 == i0)) { stop = true; break; }
+                        if (!issue_dp(g)) { stop = true; break; }
+                    }
+                    if (stop) break;
+                    if (leader) umma_commit(bar(B_KV_EMPTY));
+                    __syncwarp();
+                    const bool one = i1 - i0 == 1;
+                    if (one && !accumulators()) break;
+                    if (!issue_dv(g - 1, one) || !issue_dk(g - 1, one)) break;
                 }
-                if (stop) break;
-                if (leader) umma_commit(bar(B_KV_EMPTY));
-                __syncwarp();
-                const bool one = i1 - i0 == 1;
-                if (one && nu > 0 && !wait_bar_warp(bar(B_EPI_DONE), (nu - 1) & 1, abort, hdr, 275)) break;
-                if (!issue_dv(g - 1, one) || !issue_dk(g - 1, one)) break;
                 if (leader) umma_commit(bar(B_ACC_DONE));
                 __syncwarp();
                 ++nu;
@@ -814,8 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------------------- compute (warps 0-7)
         const int wg = warp >> 2, row = tid & 127;  // rows [64 wg, + 64) of the tiles; key of the unit
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
-        const uint32_t s_addr = lane_addr + kColST + 64 * wg, g_addr = lane_addr + kColDPT + 64 * wg;
-        const float sl2 = a.scale * kLog2e;
+        const uint32_t g_addr = lane_addr + C::kColDPT + 64 * wg;
+        const uint64_t sc2 = f2_pack(a.scale * kLog2e, a.scale * kLog2e);
         uint32_t g = 0, nu = 0, nt = 0;
         for (int it = 0;; ++it) {
             const int slot = it & 1;
@@ -833,21 +889,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.causal) v_lo = max(v_lo, key);
             const int v_hi = key < a.sinks ? (1 << 30) : key + a.left + 1;
             bool stop = false;
-            for (int i = x.i0; i < x.i1; ++i, ++g) {
-                int hq, t0, n;
-                row_tile(a, x, i, hq, t0, n);
-                const uint32_t os = g & 1;
+            RowWalk walk(a, x);
+            for (int i = x.i0; i < x.i1; ++i, ++g, walk.next(x)) {
+                const int t0 = walk.t0, n = walk.rows(x);
+                const uint32_t os = g & 1, s_addr = lane_addr + C::col_st(g) + 64 * wg;
                 // dO and the statistics (their own barrier makes the copies visible here), S^T
                 if (!wait_bar_warp(bar(B_O_FULL + os), (g >> 1) & 1, abort, hdr, 282)) { stop = true; break; }
-                if (!wait_bar_warp(bar(B_S_FULL), g & 1, abort, hdr, 283)) { stop = true; break; }
+                if (!wait_bar_warp(bar(B_S_FULL + (g & 1)), (g >> 1) & 1, abort, hdr, 283)) { stop = true; break; }
                 tc_fence_after();
-                const float4* stat = reinterpret_cast<const float4*>(smem_raw + C::oStat + os * C::kStatBytes) + 32 * wg;
+                float* stat = reinterpret_cast<float*>(smem_raw + C::oStat + os * C::kStatBytes) + 64 * wg;
                 if (n < kTile) {
                     // rows past the last: nothing of theirs (whatever was loaded) may reach a
                     // product. dP^T may still be reading dO: what it makes of these rows is masked.
                     if (row >= n) {
-                        if ((row >> 6) == wg)
-                            reinterpret_cast<float2*>(smem_raw + C::oStat + os * C::kStatBytes)[row] = make_float2(INFINITY, 0.f);
+                        if ((row >> 6) == wg) {
+                            stat[row & 63] = -INFINITY;
+                            stat[128 + (row & 63)] = 0.f;
+                        }
                         const uint32_t dst = (wg == 0 ? sQ + (g % 3) * C::kTileBytes : sDO + os * C::kTileBytes) + row * 128;
 #pragma unroll
                         for (int c = 0; c < C::kSlabs * 8; ++c)
@@ -875,18 +933,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 2; ++c) {
                     uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float4 q = stat[16 * c + e];  // two rows' (log-sum-exp, D)
-                        const float p0f = ex2(fmaf(__uint_as_float(s[32 * c + 2 * e]), sl2, -q.x));
-                        const float p1f = ex2(fmaf(__uint_as_float(s[32 * c + 2 * e + 1]), sl2, -q.z));
-                        pk[e] = pack_bf16(p0f, p1f);
-                        s[32 * c + 2 * e] = __float_as_uint(p0f);
-                        s[32 * c + 2 * e + 1] = __float_as_uint(p1f);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 q = *reinterpret_cast<const float4*>(stat + 32 * c + 2 * e);  // four rows
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t& s0 = s[32 * c + 2 * (e + h)];
+                            uint32_t& s1 = s[32 * c + 2 * (e + h) + 1];
+                            float p0, p1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s0), __uint_as_float(s1)), sc2,
+                                             h == 0 ? f2_pack(q.x, q.y) : f2_pack(q.z, q.w)), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            pk[e + h] = pack_bf16(p0, p1);
+                            s0 = __float_as_uint(p0);
+                            s1 = __float_as_uint(p1);
+                        }
                     }
                     tmem_st16(s_addr + 16 * c, pk);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(bar(c == 0 ? B_P_HALF : B_P_FULL));
+                    mbar_arrive(bar((c == 0 ? B_P_HALF : B_P_FULL) + int(g & 1)));
                 }
                 if (!wait_bar_warp(bar(B_DP_FULL), g & 1, abort, hdr, 285)) { stop = true; break; }
                 tc_fence_after();
@@ -901,10 +967,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(g_addr + 32 * c, d);
                     tmem_wait_ld_regs(d);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float4 q = stat[16 * c + e];
-                        pk[e] = pack_bf16(__uint_as_float(s[32 * c + 2 * e]) * (__uint_as_float(d[2 * e]) - q.y),
-                                          __uint_as_float(s[32 * c + 2 * e + 1]) * (__uint_as_float(d[2 * e + 1]) - q.w));
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 q = *reinterpret_cast<const float4*>(stat + 128 + 32 * c + 2 * e);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int i0 = 2 * (e + h);
+                            float d0, d1;
+                            f2_unpack(f2_mul(f2_pack(__uint_as_float(s[32 * c + i0]), __uint_as_float(s[32 * c + i0 + 1])),
+                                             f2_add(f2_pack(__uint_as_float(d[i0]), __uint_as_float(d[i0 + 1])),
+                                                    h == 0 ? f2_pack(q.x, q.y) : f2_pack(q.z, q.w))), d0, d1);
+                            pk[e + h] = pack_bf16(d0, d1);
+                        }
                     }
                     tmem_st16(g_addr + 16 * c, pk);
                 }
@@ -932,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c0 = 0; c0 < HC; c0 += 32) {
                     uint32_t o[32];
                     if (some) {
-                        tmem_ld32(lane_addr + (t == 0 ? kColDV : kColDK) + wg * HC + c0, o);
+                        tmem_ld32(lane_addr + (t == 0 ? C::kColDV : C::kColDK) + wg * HC + c0, o);
                         tmem_wait_ld_regs(o);
                     }
                     if (x.part >= 0) {
@@ -1018,11 +1091,12 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     const int sms = sm_count();
     const int64_t qrows = int64_t(a.B) * a.Hq * a.Lq, krows = int64_t(a.B) * a.Hk * a.Lk;
     int32_t* work = reinterpret_cast<int32_t*>(ws + p.work);
-    float2* stats = reinterpret_cast<float2*>(ws + p.stats);
+    float* nl2 = reinterpret_cast<float*>(ws + p.nl2);
+    float* nd = reinterpret_cast<float*>(ws + p.nd);
     float* parts = reinterpret_cast<float*>(ws + p.part);
-    const int64_t want = ((qrows + int64_t(a.B) * a.Hq + 128) * (D / 8) + 255) / 256, most = int64_t(sms) * 16;
+    const int64_t want = ((int64_t(a.B) * a.Hq * stat_rows(a.Lq) + 128) * (D / 8) + 255) / 256, most = int64_t(sms) * 16;
     window_stats_kernel<D><<<int(want < most ? want : most), 256, 0, s>>>(
-        a, static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(dO), lse, stats, work);
+        a, static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(dO), lse, nl2, nd, work);
     CUtensorMap tmQ, tmDO, tmK, tmV;
     if (krows > 0) {
         if (!make_tmap(&tmK, K, D, krows) || !make_tmap(&tmV, V, D, krows)) return cudaErrorInvalidValue;
@@ -1035,7 +1109,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         if (e != cudaSuccess) return e;
         const int nqt = (a.Lq + kTile - 1) / kTile, n = a.B * a.Hq * nqt;
         dq::window_dq_kernel<D><<<n < sms ? n : sms, dq::kThreads, smem, s>>>(
-            tmQ, tmDO, tmK, tmV, a, n, nqt, stats, work, hdr, static_cast<__nv_bfloat16*>(dQ));
+            tmQ, tmDO, tmK, tmV, a, n, nqt, nl2, nd, work, hdr, static_cast<__nv_bfloat16*>(dQ));
     }
     if (krows > 0) {
         const int smem = dkv::Cfg<D>::kSmem;
@@ -1045,7 +1119,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         const int n = heads * (p.key_tiles - p.split_tiles + p.split_tiles * p.splits);
         if (qrows == 0) tmQ = tmDO = tmK;  // no row tile is loaded
         dkv::window_dkv_kernel<D><<<n < sms ? n : sms, dkv::kThreads, smem, s>>>(
-            tmK, tmV, tmQ, tmDO, a, p, n, stats, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK),
+            tmK, tmV, tmQ, tmDO, a, p, n, nl2, nd, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK),
             static_cast<__nv_bfloat16*>(dV));
         if (p.splits > 1) {
             const int64_t blocks = (int64_t(p.split_tiles) * heads * 2 * 128 * (D / 4) + 255) / 256;
@@ -1062,8 +1136,10 @@ WinBwdPlan plan_window_bwd(const WinArgs& a, int d) {
     WinBwdPlan p;
     auto align = [](size_t x) { return (x + 255) & ~size_t(255); };
     p.work = 0;
-    p.stats = 256;
-    p.part = p.stats + align((size_t(a.B) * a.Hq * size_t((a.Lq + 1) & ~1) + 128) * 2 * sizeof(float));
+    const size_t stat = align((size_t(a.B) * a.Hq * size_t(stat_rows(a.Lq)) + 128) * sizeof(float));
+    p.nl2 = 256;
+    p.nd = p.nl2 + stat;
+    p.part = p.nd + stat;
     p.key_tiles = (a.Lk + kTile - 1) / kTile;
     const int sink_tiles = (a.sinks + kTile - 1) / kTile;
     p.split_tiles = sink_tiles < p.key_tiles ? sink_tiles : p.key_tiles;

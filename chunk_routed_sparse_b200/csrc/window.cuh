@@ -114,7 +114,8 @@ cudaError_t window_error_word(int32_t** word);
 // Workspace of the backward pass.
 struct WinBwdPlan {
     size_t work = 0;     // int32[64]: work counters of the dQ and the dK / dV kernel
-    size_t stats = 0;    // fp32 [B Hq][Lq up to even][2], + 128: log-sum-exp in exp2 units, D = dO . o
+    size_t nl2 = 0;      // fp32 [B Hq][Lq up to a multiple of 4], + 128: minus the log-sum-exp in exp2 units
+    size_t nd = 0;       // the same of minus D = - dO . o
     size_t part = 0;     // fp32 [units][2][128][d]: dV, dK parts of the split key tiles
     size_t total = 0;
     int key_tiles = 0;   // of one (b, key head)
