@@ -15,6 +15,7 @@ current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -89,14 +90,6 @@ class Rope:
 # (absent in a build of torch without CUDA; only CUDA tensors get here)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle, no Stream object
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _on(device: torch.device, fn, *args):
-    """fn(*args) with the device current."""
-    if device.index == _current_device():
-        return fn(*args)
-    with torch.cuda.device(device):
-        return fn(*args)
 
 
 def _call(where: str, device: torch.device, *args):
@@ -324,7 +317,7 @@ def qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQo, dKo, dVo=None, out=None,
     dwq = torch.empty_like(wq) if want_dw and wq is not None else None
     dwk = torch.empty_like(wk) if want_dw and wk is not None else None
     buf, at = _strides(Q, K, dQo, dKo, dVo, dQ, dK, dV)
-    ws = _bwd_workspace(Q.device, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None
+    ws = _bwd_workspace(Q, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None
     _call("moc_qk_norm_rope_bwd", Q.device, rope.handle if rope is not None else None, _DTYPE[Q.dtype], B, Hq, Hk, L, d,
           Q.data_ptr(), at, K.data_ptr(), at + 24, _at(wq), _at(wk), code, eps, _at(p), pb, pa, dQo.data_ptr(), at + 48,
           dKo.data_ptr(), at + 72, _at(dVo), at + 96, dQ.data_ptr(), at + 120, dK.data_ptr(), at + 144, _at(dV),
@@ -332,11 +325,22 @@ def qk_norm_rope_bwd(Q, K, wq, wk, rope, pos, eps, dQo, dKo, dVo=None, out=None,
     return dQ, dK, dV, dwq, dwk
 
 
-def _bwd_workspace(device, B, Hq, Hk, L, d):
-    n = _on(device, lib().moc_qk_norm_rope_bwd_workspace_bytes, B, Hq, Hk, L, d)
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(where: str, device: torch.device, *problem) -> int:
+    """lib().<where>(*problem) on the device (a size depends on the problem and the device alone)."""
+    if device.index == _current_device():
+        n = int(getattr(lib(), where)(*problem))
+    else:
+        with torch.cuda.device(device):
+            n = int(getattr(lib(), where)(*problem))
     if n == 0:
         raise ValueError("invalid problem for the workspace size query")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return n
+
+
+def _bwd_workspace(like, B, Hq, Hk, L, d):
+    n = _workspace_bytes("moc_qk_norm_rope_bwd_workspace_bytes", like.device, B, Hq, Hk, L, d)
+    return like.new_empty(n, dtype=torch.uint8)
 
 
 def _packed(qkv, Hq: int, Hk: int):
@@ -379,7 +383,7 @@ def qkv_norm_rope_bwd(qkv, Hq: int, Hk: int, wq, wk, rope, pos, eps, dQ, dK, dV,
     dqkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
     dwq = torch.empty_like(wq) if want_dw and wq is not None else None
     dwk = torch.empty_like(wk) if want_dw and wk is not None else None
-    ws = _bwd_workspace(dev, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None
+    ws = _bwd_workspace(qkv, B, Hq, Hk, L, d) if dwq is not None or dwk is not None else None
     sb, sl, sh, _ = qkv.stride()
     heads = Hq + 2 * Hk
     ob, ol = L * heads * d, heads * d

@@ -21,7 +21,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _check, lib
-from .rows import _at, _call, _on
+from .rows import _at, _call, _workspace_bytes
 
 
 def _tensor(name, x, shape, device, dtype=torch.bfloat16):
@@ -102,11 +102,9 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
     dK = (torch.empty_like(K) if fill or kv_len is None else torch.zeros_like(K)) if dK is None else dK
     dV = (torch.empty_like(K) if fill or kv_len is None else torch.zeros_like(K)) if dV is None else dV
     if ws is None:
-        n = _on(Q.device, lib().moc_window_attention_bwd_workspace_bytes, B, Hq, Hk, Lq, Lk, d, left, right, sinks,
-                1 if causal else 0)
-        if n == 0:
-            raise ValueError("invalid problem for the backward workspace size query")
-        ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+        n = _workspace_bytes("moc_window_attention_bwd_workspace_bytes", Q.device, B, Hq, Hk, Lq, Lk, d, left, right,
+                             sinks, 1 if causal else 0)
+        ws = Q.new_empty(n, dtype=torch.uint8)
     elif ws.device != Q.device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on {Q.device}")
     _call("moc_window_attention_bwd", Q.device, B, Hq, Hk, Lq, Lk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
