@@ -550,10 +550,10 @@ int sm_count() {
 // Token tiles on x (at most `most`, CTAs stride over the rest), heads split on y
 // only while that gives fewer than eight CTAs an SM: a split forms the token's
 // cosines again.
-static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t most, int* heads_per_cta) {
-    const int64_t tpc = kThreads * 8 / d, want = 8 * int64_t(sm_count());
+static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t want, int64_t most, int* heads_per_cta) {
+    const int64_t tpc = kThreads * 8 / d;
     int64_t tiles = (tokens + tpc - 1) / tpc;
-    int64_t split = tiles >= want ? 1 : (want + tiles - 1) / tiles;
+    int64_t split = tiles >= want ? 1 : want / tiles;
     if (split > heads) split = heads;
     *heads_per_cta = int((heads + split - 1) / split);
     if (tiles > most) tiles = most;
@@ -561,12 +561,13 @@ static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t most, int* heads
 }
 
 static dim3 rows_bwd_grid(int d, int64_t tokens, int heads, int* heads_per_cta) {
-    return rows_grid(d, tokens, heads, kBwdCtas * int64_t(sm_count()), heads_per_cta);
+    const int64_t n = kBwdCtas * int64_t(sm_count());
+    return rows_grid(d, tokens, heads, n, n, heads_per_cta);
 }
 
 cudaError_t launch_rows_fwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
     RowArgs a = args;
-    const dim3 grid = rows_grid(d, a.tokens, a.heads, INT64_MAX, &a.heads_per_cta);
+    const dim3 grid = rows_grid(d, a.tokens, a.heads, 8 * int64_t(sm_count()), INT64_MAX, &a.heads_per_cta);
 #define MOC_CALL(T, D, HALF, AL) rows_fwd_kernel<T, D, HALF, AL><<<grid, kThreads, 0, s>>>(a)
     MOC_ROWS_DISPATCH(MOC_CALL);
 #undef MOC_CALL
