@@ -68,6 +68,7 @@ constexpr int kThreads = 384;
 // the loading / issuing one 72: 2 x 128 x 216 + 128 x 72 = 64512
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kRowsItem = 256;
 constexpr float kLazy = 8.f;  // O is rescaled once the row max grows by more than 2^8
 
 template <int D>
@@ -118,15 +119,15 @@ struct QTile {
 
 // Items of one position range lie next to each other over the heads; the last rows
 // (the longest spans under an open causal window) come first.
-__device__ __forceinline__ void decode(const WinArgs& a, int rows, int item, Item& x) {
-    const int nqt = (a.Lq + rows - 1) / rows;
+__device__ __forceinline__ void decode(const WinArgs& a, int item, Item& x) {
+    const int nqt = (a.Lq + kRowsItem - 1) / kRowsItem;
     const int heads = a.B * a.Hq;
     const int qt = nqt - 1 - item / heads, bh = item % heads;
     x.b = bh / a.Hq;
     x.hq = bh - x.b * a.Hq;
-    x.t0 = qt * rows;
+    x.t0 = qt * kRowsItem;
     x.seq = win::seq(a, x.b);
-    x.end = min(x.t0 + rows, x.seq.m);
+    x.end = min(x.t0 + kRowsItem, x.seq.m);
     x.all = win::Span{0, 0, 0, 0, 0};
     if (x.end > x.t0) x.all = win::span(a, x.seq, x.t0, x.end);
     x.tiles = x.all.na + x.all.nb;
@@ -154,7 +155,7 @@ __device__ __forceinline__ int nth_item(int k) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WinArgs a, int n_items, int rows_item,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WinArgs a, int n_items,
                       __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int item = nth_item(k);
                 if (item >= n_items) continue;
                 Item x;
-                decode(a, rows_item, item, x);
+                decode(a, item, x);
                 const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
                 const int qrow = (x.b * a.Hq + x.hq) * a.Lq + x.t0;
                 const int krow = (x.b * a.Hk + x.hq / a.group) * a.Lk;
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int item = nth_item(k);
                 if (item >= n_items) continue;
                 Item x;
-                decode(a, rows_item, item, x);
+                decode(a, item, x);
                 const QTile qt[2] = {tile_of(a, x, 0), tile_of(a, x, 1)};
                 const int tiles = uniform(x.tiles);
                 bool have[2] = {false, false};
@@ -357,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int item = nth_item(k);
             if (item >= n_items) continue;
             Item x;
-            decode(a, rows_item, item, x);
+            decode(a, item, x);
             const QTile qt = tile_of(a, x, q);
             // rows to write: the live ones, and with a.fill those past the last
-            const int rows_out = a.fill ? min(128, min(a.Lq, x.t0 + rows_item) - x.t0 - 128 * q) : qt.rows;
+            const int rows_out = a.fill ? min(128, a.Lq - x.t0 - 128 * q) : qt.rows;
             if (rows_out <= 0) {
                 gt += x.tiles;
                 continue;
@@ -533,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void* V, void* O, float* lse,
-                     cudaStream_t s) {
+cudaError_t launch_d(const WinArgs& a, int n_items, int sms, const void* Q, const void* K, const void* V, void* O,
+                     float* lse, cudaStream_t s) {
     CUtensorMap tmQ, tmK, tmV;
     const int64_t qrows = int64_t(a.B) * a.Hq * a.Lq, krows = int64_t(a.B) * a.Hk * a.Lk;
     if (!make_tmap(&tmQ, Q, D, qrows)) return cudaErrorInvalidValue;
@@ -543,20 +544,8 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     const int smem = Cfg<D>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // Two row tiles an item keep the tensor core busy and share their keys; while that
-    // leaves half of the SMs without an item, one tile each ends sooner (the tiny scene,
-    // 18 items or 34: 18.3 against 14.5 us).
-    int rows_item = 256;
-    int n_items = a.B * a.Hq * ((a.Lq + rows_item - 1) / rows_item);
-    if (2 * n_items <= sms) {
-        rows_item = 128;
-        n_items = a.B * a.Hq * ((a.Lq + rows_item - 1) / rows_item);
-    }
     window_fwd_kernel<D><<<n_items < sms ? n_items : sms, kThreads, smem, s>>>(
-        tmQ, tmK, tmV, a, n_items, rows_item, static_cast<__nv_bfloat16*>(O), lse);
+        tmQ, tmK, tmV, a, n_items, static_cast<__nv_bfloat16*>(O), lse);
     return cudaGetLastError();
 }
 
@@ -564,7 +553,19 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
 
 cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
                               float* lse, cudaStream_t s) {
-    return d == 128 ? launch_d<128>(a, Q, K, V, O, lse, s) : launch_d<64>(a, Q, K, V, O, lse, s);
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int n_items = a.B * a.Hq * ((a.Lq + kRowsItem - 1) / kRowsItem);
+    // Two row tiles an item keep the tensor core busy and share their keys (the single-shot
+    // clip's 1,572 items: 661 against 788 us); up to three items for two SMs the one-tile
+    // kernel's shorter chain and finer items end sooner (2,112 tokens, window 256 + 64, d = 64:
+    // 18 items 14.9 -> 11.8 us, 81 items 18.5 -> 13.7, 162 items 27.1 -> 20.6, 216 items
+    // 35.4 -> 27.9; open and causal, 33 to 34 us: 108 items -> 22.8, 216 items -> 37.4; at 360
+    // and 408 items the two are level or this one ahead by up to 18 %).
+    if (n_items <= sms + sms / 2) return launch_window_tile(a, d, Q, K, V, O, lse, s);
+    return d == 128 ? launch_d<128>(a, n_items, sms, Q, K, V, O, lse, s)
+                    : launch_d<64>(a, n_items, sms, Q, K, V, O, lse, s);
 }
 
 }  // namespace moc

@@ -130,6 +130,10 @@ cudaError_t launch_window_bwd(const WinArgs& a, int d, const void* Q, const void
 cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
                               float* lse, cudaStream_t s);
 
+// The same, one 128-row tile an item: called by launch_window_fwd for few row tiles.
+cudaError_t launch_window_tile(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
+                               float* lse, cudaStream_t s);
+
 // Few rows against a cache: Lq * group <= kWinFewRows, B * Hk <= 65535, Lk > 0.
 constexpr int kWinFewRows = 16;
 cudaError_t launch_window_few(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,

@@ -201,6 +201,56 @@ def test_gradient_matches_the_definition(case):
     assert torch.equal(some[0], new[0]) and torch.equal(some[2], new[2])
 
 
+MANY = [  # more row tiles than the one-tile kernel takes; the last: several of its items a CTA
+    (6, 24, 8, 513, 513, 64, 100, 0, 3, True, [513, 0, 1, 200, 256, 400], [513, 0, 1, 200, 256, 400]),
+    (3, 25, 5, 700, 900, 128, 129, 129, 200, False, None, None),
+    (2, 40, 40, 577, 577, 128, -1, 0, 0, True, None, None),
+    (1, 250, 1, 300, 100, 64, 20, 0, 4, True, None, None),
+    (8, 30, 10, 130, 700, 64, 64, 64, 7, False, [130, 1, 0, 129, 128, 7, 64, 130], [700, 1, 3, 0, 128, 699, 64, 130]),
+    (3, 9, 3, 1425, 1425, 64, 256, 256, 64, False, None, [1425, 0, 700]),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_forward_and_gradient_of_many_row_tiles(case):
+    test_forward_matches_the_definition(case)
+    test_gradient_matches_the_definition(case)
+
+
+def test_many_row_tiles_ignore_garbage_past_the_lengths():
+    B, H, L, d = 4, 32, 400, 128
+    Q, K, V = _qkv(B, H, H, L, L, d)
+    n = _lens([170, 301, 0, 400])
+    want = moc.window_attention_fwd(Q, K, V, 60, 0, 4, True, n, n)
+    for bad in (math.nan, math.inf):
+        q, k, v = Q.clone(), K.clone(), V.clone()
+        for b in range(B):
+            for t in (q, k, v):
+                t[b, :, int(n[b]):] = bad
+        for _ in range(5):
+            got = moc.window_attention_fwd(q, k, v, 60, 0, 4, True, n, n)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_both_forward_kernels_give_a_row_the_same_weights():
+    """One head of many against the head by itself: other tiles and another order of the
+    sums, so within the rounding of P and O (each of the two within its bound)."""
+    B, H, L, d = 1, 120, 500, 64
+    Q, K, V = _qkv(B, H, H, L, L, d)
+    Q[:, 7] *= 16
+    args = (130, 40, 9, False)
+    O, lse = moc.window_attention_fwd(Q, K, V, *args)
+    for h in (0, 7, 119):
+        o, l1 = moc.window_attention_fwd(*(t[:, h:h + 1].contiguous() for t in (Q, K, V)), *args)
+        ref = W.attention(*(t[:, h:h + 1] for t in (Q, K, V)), *args)
+        # scores of head 7 are 16 times larger: so is the error of the exponents
+        w = WT * (16 if h == 7 else 1)
+        tol = U * ref["O"].abs() + (U + w) * ref["sO"]
+        for x, y in ((O[:, h:h + 1], lse[:, h:h + 1]), (o, l1)):
+            assert ((x.double() - ref["O"]).abs() <= tol).all()
+            assert ((y.double() - ref["lse"]).abs() <= 3e-4 * (16 if h == 7 else 1)).all()
+
+
 def test_gradients_with_shared_first_keys_split_over_many_rows():
     """First keys seen by thousands of rows of six query heads: their tiles' rows are
     split over units and joined."""
