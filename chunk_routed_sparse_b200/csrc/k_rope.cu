@@ -547,9 +547,10 @@ int sm_count() {
 
 }  // namespace
 
-// Token tiles on x (at most `most`, CTAs stride over the rest), heads split on y
-// only while that gives fewer than eight CTAs an SM: a split forms the token's
-// cosines again.
+// Token tiles on x (at most `most`, CTAs stride over the rest), heads split on y into
+// as many shares as keep all CTAs within `want`, one round of resident ones (a second,
+// nearly empty round costs the odd padded batch's gradient 10 %: 22.2 against 20.2 us);
+// a split forms the token's cosines again.
 static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t want, int64_t most, int* heads_per_cta) {
     const int64_t tpc = kThreads * 8 / d;
     int64_t tiles = (tokens + tpc - 1) / tpc;

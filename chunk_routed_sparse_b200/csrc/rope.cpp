@@ -211,7 +211,7 @@ extern "C" size_t moc_qk_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hk, in
     const int64_t heads = int64_t(Hq) + 2 * int64_t(Hk);
     if (heads > 65535 || L > 0x7fffffff || int64_t(B) * L > 0x7fffff00) return 0;
     if (B == 0 || L == 0 || heads == 0) return 256;
-    // with or without values: the launch takes fewer partials for fewer heads, never more
+    // with or without values, whichever launch has more CTAs (a partial each)
     int n = moc::rows_bwd_ctas(d, int64_t(B) * L, int(heads));
     if (Hq + Hk > 0) {
         const int m = moc::rows_bwd_ctas(d, int64_t(B) * L, Hq + Hk);

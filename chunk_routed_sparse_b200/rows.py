@@ -62,7 +62,11 @@ class Rope:
         h = ctypes.c_void_p()
         _check(lib().moc_build_rope(ctypes.byref(desc), ctypes.byref(h)), "moc_build_rope")
         self._h = h
+        self._args = (dim, axes, theta, interleaved, scaling, factor, original_length, alpha, beta, attention_factor)
         self.dim, self.axes, self.interleaved = int(dim), axes, bool(interleaved)
+
+    def __reduce__(self):  # copies and unpickled plans (a copied or saved model's) own a plan of their own
+        return Rope, self._args
 
     @property
     def handle(self):

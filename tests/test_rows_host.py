@@ -1,6 +1,8 @@
 """Rotary plans and the row operators' argument checks, without a GPU."""
+import copy
 import ctypes
 import math
+import pickle
 
 import pytest
 import torch
@@ -40,6 +42,17 @@ def test_bad_plans_are_refused(bad):
     with pytest.raises(moc.MocError) as e:
         moc.Rope(**bad)
     assert e.value.status == 1
+
+
+def test_copied_and_unpickled_plans_own_their_handles():
+    rope = moc.Rope(44, axes=(24, 20), interleaved=False, scaling="yarn", factor=4.0, original_length=512)
+    want = rope.table()
+    others = [copy.copy(rope), copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))]
+    assert len({r.handle.value for r in (rope, *others)}) == 4
+    rope.close()
+    rope.close()
+    for r in others:
+        assert r.table() == want and (r.dim, r.axes, r.interleaved) == (44, (24, 20), False)
 
 
 def test_bad_plan_arguments_of_the_binding():
