@@ -6,7 +6,9 @@
 //   dk_u = scale sum_t ds_tu q_t,   dv_u = sum_t p_tu dO_t,
 // the sums over t also over the query heads that share u's key head. p and ds are
 // rounded to bf16 (2^-8 of each) as operands of the last products; all sums are in
-// fp32.
+// fp32. Where a query head has no more than kFineRows rows, the rest of p and ds goes
+// into the products as a second bf16 (2^-16 of each is lost): few terms average
+// nothing out (kFineRows has what was measured).
 //
 // Launches: one that forms each row's statistics (the log-sum-exp in exp2 units and
 // D) and clears the work counters; dQ (a work unit is a 128-row tile, it owns its dQ
@@ -39,6 +41,17 @@ using win::kTile;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kProbeKeys = 384;
+// Three products more for 7 in units of few tiles, whose chains hide most of them (8 x 48
+// heads of 64 rows and keys: 229 against 212 us; 3 rows of 12 heads: 39 against 36).
+// Errors against fp64 over 700 drawn problems, as multiples of the plain form's: up to
+// 1.89 at 2 rows, 1.69 at 8, 1.55 at 32, 1.53 at 64, 1.46 at 128 without it; up to 1.02
+// with it.
+constexpr int kFineRows = 64;
+
+// What two bf16 of a packed pair leave of (x, y), as bf16.
+__device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t pk) {
+    return pack_bf16(x - bf16lo(pk), y - bf16hi(pk));
+}
 
 // Row statistics, negated for the sums they enter: - log2 sum exp2 of the scores and
 // - D, rows of a head padded to a multiple of four (16-byte copies from any fourth row)
@@ -109,7 +122,8 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 //   warp 9 (one lane): S(j) = Q K(j)^T two tiles ahead, dP(j) = dO V(j)^T, and
 //          dQ += dS(j) K(j) with dS from TMEM.
 //   warps 0-7: two warpgroups, each half of a tile's keys for all 128 rows (one
-//          thread a row): dS in fp32, written as bf16 over its own half of S.
+//          thread a row): dS in fp32, written as bf16 over its own half of S (32 of the 64
+//          columns; Fine: what that leaves of it over the other 32).
 namespace dq {
 
 constexpr int kThreads = 384;
@@ -168,7 +182,7 @@ __device__ __forceinline__ void decode(const WinArgs& a, int nqt, int u, Unit& x
     x.probe = x.y.a1 + x.y.b1 - x.y.b0 <= kProbeKeys ? x.tiles : 0;
 }
 
-template <int D>
+template <int D, bool Fine>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -336,6 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int kk = 0; kk < 8; ++kk)
                                 umma_ts(tmem + kColDQ, sc + ds_col(kk), sdesc_sw128(kb + kk * 2048, C::kSlabBytes, 1024),
                                         C::kIdescDQ, kk > 0 ? 1u : acc);
+                            if constexpr (Fine) {
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)
+                                    umma_ts(tmem + kColDQ, sc + 32 + ds_col(kk), sdesc_sw128(kb + kk * 2048, C::kSlabBytes, 1024),
+                                            C::kIdescDQ, 1u);
+                            }
                         }
                         umma_commit(bar(B_K_EMPTY + ks));
                     }
@@ -436,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mask_cols(p_addr + 32 * w, win::bits(0, nsk - 32 * w) | win::bits(lo - 32 * w, hi - 32 * w), 0u);
                     tmem_wait_st();
                 }
-                uint32_t p[64], pk[32];
+                uint32_t p[64], pk[32], rest[Fine ? 32 : 1];
                 const uint64_t nd2 = f2_pack(drow, drow);
                 tmem_ld32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
                 tmem_ld32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
@@ -452,8 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float d0, d1;
                     f2_unpack(d, d0, d1);
                     pk[c] = pack_bf16(d0, d1);
+                    if constexpr (Fine) rest[c] = pack_rest(d0, d1, pk[c]);
                 }
                 tmem_st32(s_addr, pk);
+                if constexpr (Fine) tmem_st32(s_addr + 32, rest);
                 if (end - key0 < 128) {  // K rows past the tile's keys: zeros (S has read them)
                     if (wg == 0 && row >= end - key0) {
                         const uint32_t kr = sK + (gk % 3) * C::kTileBytes + row * 128;
@@ -642,7 +664,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-template <int D>
+template <int D, bool Fine>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
@@ -748,6 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // column (from a buffer's first) of the bf16 pairs of rows 16 kk .. + 15: warpgroup
             // kk / 4 wrote its 64 rows over the first 32 columns of its own half
             auto pcol = [](int kk) { return 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3); };
+            // Fine: what they leave of P^T in the half's other 32 columns, and of dS^T, whose
+            // pairs take 16 of the 32 columns that dP^T of the same rows had, in the other 16
+            auto gcol = [&](int kk) { return Fine ? 64u * uint32_t(kk >> 2) + 32u * uint32_t((kk >> 1) & 1) + 8u * uint32_t(kk & 1) : pcol(kk); };
             auto issue_dv = [&](uint32_t t, bool first) -> bool {  // dV += P^T dO of tile t
                 const uint32_t gb = sDO + (t & 1) * C::kTileBytes;
                 const uint32_t acc = first ? 0u : 1u;
@@ -757,9 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        if ((kk & 2) == 0)
+                        if ((kk & 2) == 0) {
                             umma_ts(tmem + C::kColDV, tmem + C::col_st(t) + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
                                     C::kIdescAcc, kk > 0 ? 1u : acc);
+                            if constexpr (Fine)
+                                umma_ts(tmem + C::kColDV, tmem + C::col_st(t) + 32 + pcol(kk),
+                                        sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024), C::kIdescAcc, 1u);
+                        }
                 }
                 __syncwarp();
                 if (!wait_bar_warp(bar(B_P_FULL + (t & 1)), (t >> 1) & 1, abort, hdr, 268)) return false;
@@ -767,9 +796,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        if ((kk & 2) != 0)
+                        if ((kk & 2) != 0) {
                             umma_ts(tmem + C::kColDV, tmem + C::col_st(t) + pcol(kk), sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024),
                                     C::kIdescAcc, 1u);
+                            if constexpr (Fine)
+                                umma_ts(tmem + C::kColDV, tmem + C::col_st(t) + 32 + pcol(kk),
+                                        sdesc_sw128(gb + kk * 2048, C::kSlabBytes, 1024), C::kIdescAcc, 1u);
+                        }
                     umma_commit(bar(B_O_EMPTY + (t & 1)));
                 }
                 __syncwarp();
@@ -782,9 +815,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
                     const uint32_t acc = first ? 0u : 1u;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ts(tmem + C::kColDK, tmem + C::kColDPT + pcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
+                    for (int kk = 0; kk < 8; ++kk) {
+                        umma_ts(tmem + C::kColDK, tmem + C::kColDPT + gcol(kk), sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024),
                                 C::kIdescAcc, kk > 0 ? 1u : acc);
+                        if constexpr (Fine)
+                            umma_ts(tmem + C::kColDK, tmem + C::kColDPT + 16 + gcol(kk),
+                                    sdesc_sw128(qb + kk * 2048, C::kSlabBytes, 1024), C::kIdescAcc, 1u);
+                    }
                     umma_commit(bar(B_Q_EMPTY + t % 3));
                 }
                 __syncwarp();
@@ -931,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld_regs(s);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[16];
+                    uint32_t pk[16], rest[Fine ? 16 : 1];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const float4 q = *reinterpret_cast<const float4*>(stat + 32 * c + 2 * e);  // four rows
@@ -945,11 +982,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p0 = ex2(p0);
                             p1 = ex2(p1);
                             pk[e + h] = pack_bf16(p0, p1);
+                            if constexpr (Fine) rest[e + h] = pack_rest(p0, p1, pk[e + h]);
                             s0 = __float_as_uint(p0);
                             s1 = __float_as_uint(p1);
                         }
                     }
                     tmem_st16(s_addr + 16 * c, pk);
+                    if constexpr (Fine) tmem_st16(s_addr + 32 + 16 * c, rest);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(bar((c == 0 ? B_P_HALF : B_P_FULL) + int(g & 1)));
@@ -963,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t d[32], pk[16];
+                    uint32_t d[32], pk[16], rest[Fine ? 16 : 1];
                     tmem_ld32(g_addr + 32 * c, d);
                     tmem_wait_ld_regs(d);
 #pragma unroll
@@ -977,9 +1016,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              f2_add(f2_pack(__uint_as_float(d[i0]), __uint_as_float(d[i0 + 1])),
                                                     h == 0 ? f2_pack(q.x, q.y) : f2_pack(q.z, q.w))), d0, d1);
                             pk[e + h] = pack_bf16(d0, d1);
+                            if constexpr (Fine) rest[e + h] = pack_rest(d0, d1, pk[e + h]);
                         }
                     }
-                    tmem_st16(g_addr + 16 * c, pk);
+                    tmem_st16(g_addr + (Fine ? 32 : 16) * c, pk);
+                    if constexpr (Fine) tmem_st16(g_addr + 32 * c + 16, rest);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1082,7 +1123,7 @@ int sm_count() {
     return sms;
 }
 
-template <int D>
+template <int D, bool Fine>
 cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void* V, const void* O, const float* lse,
                      const void* dO, void* dQ, void* dK, void* dV, char* ws, const WinBwdPlan& p, cudaStream_t s) {
     int32_t* hdr = nullptr;
@@ -1105,20 +1146,20 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         if (!make_tmap(&tmQ, Q, D, qrows) || !make_tmap(&tmDO, dO, D, qrows)) return cudaErrorInvalidValue;
         if (krows == 0) tmK = tmV = tmQ;  // no key tile is loaded
         const int smem = dq::Cfg<D>::kSmem;
-        e = cudaFuncSetAttribute(dq::window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(dq::window_dq_kernel<D, Fine>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         const int nqt = (a.Lq + kTile - 1) / kTile, n = a.B * a.Hq * nqt;
-        dq::window_dq_kernel<D><<<n < sms ? n : sms, dq::kThreads, smem, s>>>(
+        dq::window_dq_kernel<D, Fine><<<n < sms ? n : sms, dq::kThreads, smem, s>>>(
             tmQ, tmDO, tmK, tmV, a, n, nqt, nl2, nd, work, hdr, static_cast<__nv_bfloat16*>(dQ));
     }
     if (krows > 0) {
         const int smem = dkv::Cfg<D>::kSmem;
-        e = cudaFuncSetAttribute(dkv::window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(dkv::window_dkv_kernel<D, Fine>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         const int heads = a.B * a.Hk;
         const int n = heads * (p.key_tiles - p.split_tiles + p.split_tiles * p.splits);
         if (qrows == 0) tmQ = tmDO = tmK;  // no row tile is loaded
-        dkv::window_dkv_kernel<D><<<n < sms ? n : sms, dkv::kThreads, smem, s>>>(
+        dkv::window_dkv_kernel<D, Fine><<<n < sms ? n : sms, dkv::kThreads, smem, s>>>(
             tmK, tmV, tmQ, tmDO, a, p, n, nl2, nd, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK),
             static_cast<__nv_bfloat16*>(dV));
         if (p.splits > 1) {
@@ -1164,8 +1205,11 @@ WinBwdPlan plan_window_bwd(const WinArgs& a, int d) {
 cudaError_t launch_window_bwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, const void* O,
                               const float* lse, const void* dO, void* dQ, void* dK, void* dV, char* ws,
                               const WinBwdPlan& p, cudaStream_t s) {
-    if (d == 128) return launch_d<128>(a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, p, s);
-    return launch_d<64>(a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, p, s);
+    if (a.Lq <= kFineRows)
+        return d == 128 ? launch_d<128, true>(a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, p, s)
+                        : launch_d<64, true>(a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, p, s);
+    return d == 128 ? launch_d<128, false>(a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, p, s)
+                    : launch_d<64, false>(a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, p, s);
 }
 
 }  // namespace moc

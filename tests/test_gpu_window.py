@@ -251,6 +251,32 @@ def test_both_forward_kernels_give_a_row_the_same_weights():
             assert ((y.double() - ref["lse"]).abs() <= 3e-4 * (16 if h == 7 else 1)).all()
 
 
+@pytest.mark.parametrize("case", [
+    (1, 1, 1, 2, 2, 64, -1, -1, 0, False, None, None), (8, 1, 1, 5, 7, 128, -1, 0, 1, True, None, None),
+    (2, 2, 2, 4, 184, 64, 201, 0, 0, True, None, None), (1, 12, 4, 3, 1434, 128, 18, 18, 4, False, None, [1100]),
+    (3, 6, 2, 17, 300, 64, 90, 0, 130, True, [17, 0, 9], [300, 20, 150]), (2, 4, 4, 64, 64, 128, -1, -1, 0, False, None, None)],
+    ids=str)
+def test_gradients_of_few_rows_lose_little_more_than_their_own_rounding(case):
+    """Up to 64 rows a head, p and ds enter the products as two bf16: 2^-16 of each is lost
+    (u of u), not u. The rows' spans stay below 384 keys, so that D is exact in dQ too.
+    Left of the bounds above: u |x| + (2^-16 + 2 w) size for dQ and dK, + (2^-16 + w) for dV."""
+    B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, ql, kl = case
+    Q, K, V = _qkv(B, Hq, Hk, Lq, Lk, d)
+    g = _rand(B, Hq, Lq, d, seed=9)
+    ql, kl = _lens(ql), _lens(kl)
+    args = (left, right, sinks, causal, ql, kl)
+    O, lse = moc.window_attention_fwd(Q, K, V, *args)
+    ref = W.attention(Q, K, V, *args, dO=g)
+    got = moc.window_attention_bwd(Q, K, V, O, lse, g, *args)
+    for name, size, x, k in (("dQ", "sQ", got[0], 2 * WT), ("dK", "sK", got[1], 2 * WT), ("dV", "sV", got[2], WT)):
+        err = (x.double() - ref[name]).abs()
+        tol = U * ref[name].abs() + (2.0 ** -16 + k) * ref[size] + 1e-30
+        assert (err <= tol).all(), (name, float((err / tol).max()))
+    for x, y in zip(got, moc.window_attention_bwd(Q, K, V, O, lse, g, *args)):
+        assert torch.equal(x, y)
+    moc.check_window_error()
+
+
 def test_gradients_with_shared_first_keys_split_over_many_rows():
     """First keys seen by thousands of rows of six query heads: their tiles' rows are
     split over units and joined."""
