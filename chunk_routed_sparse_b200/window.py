@@ -24,8 +24,11 @@ from . import _check, lib
 from .rows import _at, _call, _workspace_bytes
 
 
+_FAR = 1 << 40
+
+
 def _tensor(name, x, shape, device, dtype=torch.bfloat16):
-    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.device != device or tuple(x.shape) != tuple(shape) or \
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.shape != shape or x.device != device or \
             not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on {device}")
 
@@ -36,24 +39,27 @@ def _problem(Q, K, V, q_len, kv_len):
     B, Hq, Lq, d = Q.shape
     if not isinstance(K, torch.Tensor) or K.dim() != 4:
         raise ValueError("K: expected a bf16 CUDA tensor [B, Hk, Lk, d]")
-    Hk, Lk = K.shape[1], K.shape[2]
+    _, Hk, Lk, _ = K.shape
     if d not in (64, 128):
         raise ValueError(f"d = {d}, expected 64 or 128")
     if (Hk == 0) != (Hq == 0) or (Hk and Hq % Hk):
         raise ValueError(f"{Hk} key heads do not divide {Hq} query heads")
-    _tensor("Q", Q, Q.shape, Q.device)
-    _tensor("K", K, (B, Hk, Lk, d), Q.device)
-    _tensor("V", V, (B, Hk, Lk, d), Q.device)
-    for name, x in (("q_len", q_len), ("kv_len", kv_len)):
-        if x is not None:
-            _tensor(name, x, (B,), Q.device, torch.int32)
+    device, keys = Q.device, (B, Hk, Lk, d)
+    _tensor("Q", Q, Q.shape, device)
+    _tensor("K", K, keys, device)
+    _tensor("V", V, keys, device)
+    if q_len is not None:
+        _tensor("q_len", q_len, (B,), device, torch.int32)
+    if kv_len is not None:
+        _tensor("kv_len", kv_len, (B,), device, torch.int32)
     return B, Hq, Hk, Lq, Lk, d
 
 
 def _limits(left, right, sinks):
     """The window's sizes in 64 bits: any negative limit is none, any huge one reaches every key."""
-    far = 1 << 40
-    return max(min(int(left), far), -1), max(min(int(right), far), -1), max(min(int(sinks), far), -1)
+    if 0 <= left < _FAR and 0 <= right < _FAR and 0 <= sinks < _FAR:
+        return int(left), int(right), int(sinks)
+    return tuple(max(min(int(x), _FAR), -1) for x in (left, right, sinks))
 
 
 def window_attention_fwd(Q, K, V, left: int = -1, right: int = -1, sinks: int = 0, causal: bool = False,
