@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const __grid_constan
     // the CTA's first rows are requested before the angles are formed
     int k0 = 0, base = 0;
     while (h_lo >= base + a.sec[k0].H) base += a.sec[k0++].H;
+    sm100::let_next_kernel_start();
+    sm100::wait_for_previous_kernel();
     Raw<T> raw[kRows];
     {
         const RowSec& sec = a.sec[k0];
@@ -343,7 +345,9 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rows_bwd_kernel(const __gr
     __shared__ __align__(16) float ws[D];
     __shared__ float red[TPC][D];
     __shared__ __align__(16) uint4 ring[AL ? ST * RS * 2 * W * kThreads : 1];
+    sm100::let_next_kernel_start();
     tab_to_smem(a, turn, axis);
+    sm100::wait_for_previous_kernel();
     const int r = threadIdx.x % LPR, e0 = 8 * r;
     const int h_lo = blockIdx.y * a.heads_per_cta, h_hi = min(h_lo + a.heads_per_cta, a.heads);
     const int64_t step = int64_t(gridDim.x) * TPC, first = int64_t(blockIdx.x) * TPC;
@@ -501,19 +505,21 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rows_bwd_kernel(const __gr
 // dw = sum of the CTAs' parts: one CTA per weight and 32 columns, 32 runs of parts
 // added in order, then the runs in order.
 template <typename W>
-__global__ void __launch_bounds__(1024) rows_dw_kernel(int ctas, int D, const float* __restrict__ part, W* dwq, W* dwk) {
+__global__ void __launch_bounds__(1024) rows_dw_kernel(int ctas, int D, const float* part, W* dwq, W* dwk) {
     __shared__ float red[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    sm100::wait_for_previous_kernel();
     W* out = blockIdx.y == 0 ? dwq : dwk;
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    const int c = blockIdx.x * 32 + tx;
     float s = 0.f;
 #pragma unroll 8
-    for (int i = threadIdx.y; i < ctas; i += 32) s += part[(size_t(i) * 2 + blockIdx.y) * D + c];
-    red[threadIdx.y][threadIdx.x] = s;
+    for (int i = ty; i < ctas; i += 32) s += part[(size_t(i) * 2 + blockIdx.y) * D + c];
+    red[ty][tx] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && out) {
+    if (ty == 0 && out) {
         s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
+        for (int i = 0; i < 32; ++i) s += red[i][tx];
         if constexpr (sizeof(W) == 4) out[c] = s;
         else if constexpr (std::is_same<W, __half>::value) out[c] = __float2half_rn(s);
         else out[c] = __float2bfloat16_rn(s);
@@ -569,10 +575,11 @@ static dim3 rows_bwd_grid(int d, int64_t tokens, int heads, int* heads_per_cta) 
 cudaError_t launch_rows_fwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
     RowArgs a = args;
     const dim3 grid = rows_grid(d, a.tokens, a.heads, 8 * int64_t(sm_count()), INT64_MAX, &a.heads_per_cta);
-#define MOC_CALL(T, D, HALF, AL) rows_fwd_kernel<T, D, HALF, AL><<<grid, kThreads, 0, s>>>(a)
+#define MOC_CALL(T, D, HALF, AL) e = sm100::launch_after(rows_fwd_kernel<T, D, HALF, AL>, grid, kThreads, 0, s, a)
+    cudaError_t e = cudaSuccess;
     MOC_ROWS_DISPATCH(MOC_CALL);
 #undef MOC_CALL
-    return cudaGetLastError();
+    return e;
 }
 
 int rows_bwd_ctas(int d, int64_t tokens, int heads) {
@@ -584,23 +591,24 @@ int rows_bwd_ctas(int d, int64_t tokens, int heads) {
 cudaError_t launch_rows_bwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
     RowArgs a = args;
     const dim3 grid = rows_bwd_grid(d, a.tokens, a.heads, &a.heads_per_cta);
-#define MOC_CALL(T, D, HALF, AL) rows_bwd_kernel<T, D, HALF, AL><<<grid, kThreads, 0, s>>>(a)
+#define MOC_CALL(T, D, HALF, AL) e = sm100::launch_after(rows_bwd_kernel<T, D, HALF, AL>, grid, kThreads, 0, s, a)
+    cudaError_t e = cudaSuccess;
     MOC_ROWS_DISPATCH(MOC_CALL);
 #undef MOC_CALL
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_rows_dw(int dtype, int w_fp32, int d, int ctas, const float* part, void* dwq, void* dwk,
                            cudaStream_t s) {
-    const dim3 grid(d / 32, 2), block(32, 32);
+    const dim3 grid(d / 32, 2);
     if (w_fp32 || dtype == MOC_FP32)
-        rows_dw_kernel<float><<<grid, block, 0, s>>>(ctas, d, part, static_cast<float*>(dwq), static_cast<float*>(dwk));
-    else if (dtype == MOC_FP16)
-        rows_dw_kernel<__half><<<grid, block, 0, s>>>(ctas, d, part, static_cast<__half*>(dwq), static_cast<__half*>(dwk));
-    else
-        rows_dw_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(ctas, d, part, static_cast<__nv_bfloat16*>(dwq),
-                                                             static_cast<__nv_bfloat16*>(dwk));
-    return cudaGetLastError();
+        return sm100::launch_after(rows_dw_kernel<float>, grid, 1024, 0, s, ctas, d, part, static_cast<float*>(dwq),
+                                   static_cast<float*>(dwk));
+    if (dtype == MOC_FP16)
+        return sm100::launch_after(rows_dw_kernel<__half>, grid, 1024, 0, s, ctas, d, part, static_cast<__half*>(dwq),
+                                   static_cast<__half*>(dwk));
+    return sm100::launch_after(rows_dw_kernel<__nv_bfloat16>, grid, 1024, 0, s, ctas, d, part,
+                               static_cast<__nv_bfloat16*>(dwq), static_cast<__nv_bfloat16*>(dwk));
 }
 
 }  // namespace moc

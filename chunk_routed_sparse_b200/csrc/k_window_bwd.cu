@@ -80,11 +80,11 @@ constexpr uint32_t kMinusInf = 0xff800000u;
 // ---- row statistics ------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant__ WinArgs a,
-                                                           const __nv_bfloat16* __restrict__ O,
-                                                           const __nv_bfloat16* __restrict__ dO,
-                                                           const float* __restrict__ lse, float* __restrict__ nl2,
-                                                           float* __restrict__ nd, int32_t* __restrict__ work) {
+                                                           const __nv_bfloat16* O, const __nv_bfloat16* dO,
+                                                           const float* lse, float* nl2, float* nd, int32_t* work) {
     constexpr int LPR = D / 8, RPC = 256 / LPR;  // lanes a row (16 bytes each), rows a step
+    let_next_kernel_start();
+    wait_for_previous_kernel();
     if (blockIdx.x == 0 && threadIdx.x < 2) work[threadIdx.x] = 0;
     const int per = int(stat_rows(a.Lq));
     const int64_t heads = int64_t(a.B) * a.Hq, total = heads * per + 128;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
                 acc = fmaf(bf16lo(xs[k]), bf16lo(ys[k]), acc);
                 acc = fmaf(bf16hi(xs[k]), bf16hi(ys[k]), acc);
             }
-            const float v = __ldg(lse + row);
+            const float v = lse[row];
             if (v > -INFINITY || v != v) l2 = -v * kLog2e;
         }
 #pragma unroll
@@ -186,13 +186,13 @@ template <int D, bool Fine>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ WinArgs a, int n_units, int nqt, const float* __restrict__ nl2,
-                     float* __restrict__ nd, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
-                     __nv_bfloat16* __restrict__ dQ) {
+                     const __grid_constant__ WinArgs a, int n_units, int nqt, const float* nl2, float* nd, int32_t* work,
+                     int32_t* hdr, __nv_bfloat16* __restrict__ dQ) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     if (base & 1023u) {
+        wait_for_previous_kernel();
         if (threadIdx.x == 0) set_error(hdr, ERR_CHECK, 230);
         return;
     }
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    let_next_kernel_start();
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) {
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
+    wait_for_previous_kernel();
 
     if (warp >= 8) {
         regs_dec<kRegsOther>();
@@ -669,12 +671,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                       const __grid_constant__ WinArgs a, const __grid_constant__ WinBwdPlan p, int n_units,
-                      const float* __restrict__ nl2, const float* __restrict__ nd, int32_t* __restrict__ work, int32_t* __restrict__ hdr,
-                      float* __restrict__ parts, __nv_bfloat16* __restrict__ dK, __nv_bfloat16* __restrict__ dV) {
+                      const float* nl2, const float* nd, int32_t* work, int32_t* hdr, float* parts, __nv_bfloat16* __restrict__ dK, __nv_bfloat16* __restrict__ dV) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     if (base & 1023u) {
+        wait_for_previous_kernel();
         if (threadIdx.x == 0) set_error(hdr, ERR_CHECK, 260);
         return;
     }
@@ -684,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    let_next_kernel_start();
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) {
@@ -705,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
+    wait_for_previous_kernel();
 
     if (warp >= 8) {
         regs_dec<kRegsOther>();
@@ -1089,10 +1093,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) window_dkv_join_kernel(const __grid_constant__ WinArgs a,
                                                               const __grid_constant__ WinBwdPlan p,
-                                                              const float* __restrict__ parts,
-                                                              __nv_bfloat16* __restrict__ dK,
-                                                              __nv_bfloat16* __restrict__ dV) {
+                                                              const float* parts, __nv_bfloat16* dK, __nv_bfloat16* dV) {
     constexpr int PER = D / 4;
+    wait_for_previous_kernel();
     const int heads = a.B * a.Hk;
     const int64_t total = int64_t(p.split_tiles) * heads * 2 * 128 * PER;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
@@ -1136,8 +1139,9 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     float* nd = reinterpret_cast<float*>(ws + p.nd);
     float* parts = reinterpret_cast<float*>(ws + p.part);
     const int64_t want = ((int64_t(a.B) * a.Hq * stat_rows(a.Lq) + 128) * (D / 8) + 255) / 256, most = int64_t(sms) * 16;
-    window_stats_kernel<D><<<int(want < most ? want : most), 256, 0, s>>>(
-        a, static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(dO), lse, nl2, nd, work);
+    e = launch_after(window_stats_kernel<D>, int(want < most ? want : most), 256, 0, s, a,
+                     static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(dO), lse, nl2, nd, work);
+    if (e != cudaSuccess) return e;
     CUtensorMap tmQ, tmDO, tmK, tmV;
     if (krows > 0) {
         if (!make_tmap(&tmK, K, D, krows) || !make_tmap(&tmV, V, D, krows)) return cudaErrorInvalidValue;
@@ -1149,8 +1153,9 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         e = cudaFuncSetAttribute(dq::window_dq_kernel<D, Fine>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         const int nqt = (a.Lq + kTile - 1) / kTile, n = a.B * a.Hq * nqt;
-        dq::window_dq_kernel<D, Fine><<<n < sms ? n : sms, dq::kThreads, smem, s>>>(
-            tmQ, tmDO, tmK, tmV, a, n, nqt, nl2, nd, work, hdr, static_cast<__nv_bfloat16*>(dQ));
+        e = launch_after(dq::window_dq_kernel<D, Fine>, n < sms ? n : sms, dq::kThreads, smem, s, tmQ, tmDO, tmK, tmV, a, n,
+                         nqt, nl2, nd, work, hdr, static_cast<__nv_bfloat16*>(dQ));
+        if (e != cudaSuccess) return e;
     }
     if (krows > 0) {
         const int smem = dkv::Cfg<D>::kSmem;
@@ -1159,13 +1164,14 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         const int heads = a.B * a.Hk;
         const int n = heads * (p.key_tiles - p.split_tiles + p.split_tiles * p.splits);
         if (qrows == 0) tmQ = tmDO = tmK;  // no row tile is loaded
-        dkv::window_dkv_kernel<D, Fine><<<n < sms ? n : sms, dkv::kThreads, smem, s>>>(
-            tmK, tmV, tmQ, tmDO, a, p, n, nl2, nd, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK),
-            static_cast<__nv_bfloat16*>(dV));
+        e = launch_after(dkv::window_dkv_kernel<D, Fine>, n < sms ? n : sms, dkv::kThreads, smem, s, tmK, tmV, tmQ, tmDO, a,
+                         p, n, nl2, nd, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV));
+        if (e != cudaSuccess) return e;
         if (p.splits > 1) {
             const int64_t blocks = (int64_t(p.split_tiles) * heads * 2 * 128 * (D / 4) + 255) / 256;
-            dkv::window_dkv_join_kernel<D><<<int(blocks < most ? blocks : most), 256, 0, s>>>(
-                a, p, parts, static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV));
+            e = launch_after(dkv::window_dkv_join_kernel<D>, int(blocks < most ? blocks : most), 256, 0, s, a, p, parts,
+                             static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV));
+            if (e != cudaSuccess) return e;
         }
     }
     return cudaGetLastError();

@@ -12,11 +12,13 @@
 //          MMAs (mma.sync; 16 rows fill its M, a 128-row tcgen05 tile would be an
 //          eighth used at best, and the bytes bound this kernel either way), running
 //          maximum and sum per warp in fp32; joined over the warps at the end.
-// One token of eight streams, 24 heads, 8,255 visible keys each (811 MB): 126 us, the
+// One token of eight streams, 24 heads, 8,255 visible keys each (811 MB): 125 us, the
 // measured copy bandwidth. A fourth stage (one CTA an SM) takes 202 us; clusters of 1,
 // 2, 4 and 8 CTAs 131, 153, 129 and 144 us.
 // Rounding and masking as in the many-row kernel: P to bf16 before P V, sums of the
-// unrounded weights, keys past a run of visible ones never reach a product.
+// unrounded weights, keys past a run of visible ones never reach a product. (The rest of P
+// as a second operand: errors of O 1.00 instead of 1.35 times its own rounding's, for 2 to
+// 6 % of the time, 124.5 -> 127.4 us here. Not taken.)
 #include "common.cuh"
 #include "pipeline.cuh"
 #include "tmap.cuh"
@@ -46,7 +48,7 @@ struct Cfg {
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     window_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __grid_constant__ WinArgs a, const __nv_bfloat16* __restrict__ Q,
+                      const __grid_constant__ WinArgs a, const __nv_bfloat16* Q,
                       __nv_bfloat16* __restrict__ O, float* __restrict__ lse, int32_t* __restrict__ hdr) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -58,6 +60,7 @@ __global__ void __launch_bounds__(kThreads)
     auto empty = [&](int s) { return sBar + 16u * uint32_t(s) + 8u; };
     volatile int* abort = reinterpret_cast<volatile int*>(gbase + C::oBar + 96);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    sm100::let_next_kernel_start();
     const int rank = int(cluster_rank()), cs = int(gridDim.x);  // a cluster spans the grid's x
     const int bh = blockIdx.y, b = bh / a.Hk, hk = bh - b * a.Hk;
 
@@ -70,6 +73,7 @@ __global__ void __launch_bounds__(kThreads)
         fence_mbar_init();
     }
     __syncthreads();
+    sm100::wait_for_previous_kernel();
 
     const win::Seq seq = win::seq(a, b);
     win::Span y{0, 0, 0, 0, 0};
@@ -344,13 +348,15 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = unsigned(cs);
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // wait_for_previous_kernel
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, window_few_kernel<D>, tmK, tmV, a, static_cast<const __nv_bfloat16*>(Q),
                            static_cast<__nv_bfloat16*>(O), lse, hdr);
     return e != cudaSuccess ? e : cudaGetLastError();

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t* const hdr = g_window_err;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    let_next_kernel_start();
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1 || x >= B_P_HALF) ? 128 : 1);
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
+    wait_for_previous_kernel();
     const int n_rounds = (n_items + int(gridDim.x) - 1) / int(gridDim.x);
 
     if (warp >= 8) {
@@ -544,9 +546,8 @@ cudaError_t launch_d(const WinArgs& a, int n_items, int sms, const void* Q, cons
     const int smem = Cfg<D>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    window_fwd_kernel<D><<<n_items < sms ? n_items : sms, kThreads, smem, s>>>(
-        tmQ, tmK, tmV, a, n_items, static_cast<__nv_bfloat16*>(O), lse);
-    return cudaGetLastError();
+    return launch_after(window_fwd_kernel<D>, n_items < sms ? n_items : sms, kThreads, smem, s, tmQ, tmK, tmV, a,
+                        n_items, static_cast<__nv_bfloat16*>(O), lse);
 }
 
 }  // namespace

@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     if (base & 1023u) {
+        wait_for_previous_kernel();
         if (threadIdx.x == 0) set_error(hdr, ERR_CHECK, 310);
         return;
     }
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    let_next_kernel_start();
 
     if (tid == 0) {
         for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1 || x == B_EX) ? 256 : 1);
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
+    wait_for_previous_kernel();
     const int n_rounds = (n_items + int(gridDim.x) - 1) / int(gridDim.x);
 
     if (warp >= 8) {
@@ -424,9 +427,8 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int nqt = (a.Lq + 127) / 128, n_items = a.B * a.Hq * nqt;
-    window_tile_kernel<D><<<n_items < sms ? n_items : sms, kThreads, smem, s>>>(
-        tmQ, tmK, tmV, a, n_items, nqt, hdr, static_cast<__nv_bfloat16*>(O), lse);
-    return cudaGetLastError();
+    return launch_after(window_tile_kernel<D>, n_items < sms ? n_items : sms, kThreads, smem, s, tmQ, tmK, tmV,
+                        a, n_items, nqt, hdr, static_cast<__nv_bfloat16*>(O), lse);
 }
 
 }  // namespace
