@@ -119,9 +119,9 @@ def _rows(name: str, x: torch.Tensor, like: Optional[torch.Tensor] = None, shape
         raise ValueError(f"{name}: d = {x.shape[3]}, expected 64 or 128")
     if x.stride(3) != 1 and x.numel():
         raise ValueError(f"{name}: the last dim has stride {x.stride(3)}, expected 1")
-    if like is not None and (x.dtype != like.dtype or x.device != like.device):
+    if like is not None and (x.dtype is not like.dtype or x.device != like.device):
         raise ValueError(f"{name}: {x.dtype} on {x.device}, expected {like.dtype} on {like.device}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
 
 
@@ -140,15 +140,16 @@ def _positions(rope: Optional[Rope], pos: Optional[torch.Tensor], B: int, L: int
         if n != 1:
             raise ValueError(f"a rotation over {n} axes needs positions")
         return None, 0, 0
-    if pos.dtype != torch.int32 or pos.device != device:
+    if pos.dtype is not torch.int32 or pos.device != device:
         raise ValueError(f"pos: {pos.dtype} on {pos.device}, expected int32 on {device}")
-    shape = tuple(pos.shape)
-    ok = shape == (L,) and n == 1 or shape == (n, L) or shape == (B, n, L)
+    shape = pos.shape
+    ok = shape == (B, n, L) or shape == (n, L) or shape == (L,) and n == 1
     if not ok:
-        raise ValueError(f"pos: shape {shape}, expected [L], [axes, L] or [B, axes, L] for B = {B}, axes = {n}, L = {L}")
+        raise ValueError(f"pos: shape {tuple(shape)}, expected [L], [axes, L] or [B, axes, L] for B = {B}, axes = {n}, L = {L}")
     if L > 1 and pos.stride(-1) != 1:
         raise ValueError("pos: the last dim is not dense")
-    return pos, pos.stride(0) if pos.dim() == 3 else 0, pos.stride(-2) if pos.dim() > 1 else 0
+    dims = len(shape)
+    return pos, pos.stride(0) if dims == 3 else 0, pos.stride(-2) if dims > 1 else 0
 
 
 _stride_arrays: dict = {}  # strides -> their host array and its address (read during a call only)
@@ -247,16 +248,20 @@ def rotary(rope: Rope, X: torch.Tensor, pos: Optional[torch.Tensor] = None) -> t
 def _weights(wq, wk, X, d):
     """The weights' common type code."""
     code = 2
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is None:
-            continue
-        if tuple(w.shape) != (d,) or not w.is_contiguous() or w.device != X.device or \
-                w.dtype not in (torch.float32, X.dtype):
-            raise ValueError(f"{name}: expected a contiguous [{d}] tensor in fp32 or {X.dtype} on {X.device}")
-        code = _DTYPE[w.dtype]
-    if wq is not None and wk is not None and wq.dtype != wk.dtype:
-        raise ValueError("wq and wk have different types")
+    if wq is not None:
+        code = _weight("wq", wq, X, d)
+    if wk is not None:
+        code = _weight("wk", wk, X, d)
+        if wq is not None and wq.dtype is not wk.dtype:
+            raise ValueError("wq and wk have different types")
     return code
+
+
+def _weight(name, w, X, d):
+    if w.shape != (d,) or not w.is_contiguous() or w.device != X.device or \
+            w.dtype is not torch.float32 and w.dtype is not X.dtype:
+        raise ValueError(f"{name}: expected a contiguous [{d}] tensor in fp32 or {X.dtype} on {X.device}")
+    return _DTYPE[w.dtype]
 
 
 def qk_norm_rope_fwd(Q, K, V=None, wq=None, wk=None, rope: Optional[Rope] = None,
@@ -428,7 +433,8 @@ def qkv_norm_rope(qkv: torch.Tensor, Hq: int, Hk: int, wq: Optional[torch.Tensor
                   pos: Optional[torch.Tensor] = None, eps: float = 1e-6):
     """Differentiable: the packed projection [B, L, Hq + 2 Hk, d] to head-major Q
     (normalised, rotated), K (the same) and V in one pass."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (qkv, wq, wk)):
+    if torch.is_grad_enabled() and (qkv.requires_grad or wq is not None and wq.requires_grad or
+                                    wk is not None and wk.requires_grad):
         return QKVNormRope.apply(qkv, wq, wk, Hq, Hk, rope, pos, eps)
     return qkv_norm_rope_fwd(qkv, Hq, Hk, wq, wk, rope, pos, eps)
 
