@@ -18,7 +18,7 @@
 // more registers than it gives, and addressing every row anew costs 8 % (a third of
 // the issue slots are in use). Outputs are streaming stores: nothing here reads them.
 // At the measured copy bandwidth: the eight-shot projection (6.65 GB) in 1.03-1.05 ms;
-// the single-shot rotation (204 MB in, 204 MB out) in 36 us against 32 us.
+// the single-shot rotation (102 MB in, 102 MB out) in 35 us against 32 us.
 //
 // Angles: the position times a 64-bit fraction of a turn, modulo 2^64, is exact
 // for every 32-bit position (an fp32 product loses 0.01 rad at position 180,000);
