@@ -208,3 +208,73 @@ def test_offsets_past_32_bits():
     small = moc.qkv_norm_rope(qkv[:, -3:], 24, 24, None, None, rope, pos)
     for x, y in zip((Q, K, V), small):
         assert torch.equal(x[:, :, -3:], y) and (x[:, :, :-3] == 0).all()
+
+
+def test_kernels_that_start_early_wait_for_all_that_they_depend_on():
+    """Front end, attention and gradients on two streams that fork and join, buffers
+    overwritten right before and right after, eagerly and in a captured graph: the same
+    bits as one call after the other."""
+    B, Hq, Hk, L, d = 2, 8, 4, 1300, 64
+    rope = moc.Rope(d, interleaved=False)
+    w = 1 + 0.1 * _rand(d, seed=60, dtype=torch.float32)
+    src = [_rand(B, L, Hq + 2 * Hk, d, seed=61 + i) for i in range(2)]
+    up = _rand(B, Hq, L, d, seed=64)
+    args = (200, 0, 140, True)
+    qkv, half = torch.empty_like(src[0]), torch.empty_like(src[0])
+
+    def chain(x):
+        Q, K, V = moc.qkv_norm_rope(x, Hq, Hk, w, w, rope)
+        O, lse = moc.window_attention_fwd(Q, K, V, *args)
+        g = moc.window_attention_bwd(Q, K, V, O, lse, up, *args)
+        return (O, lse, *g, *moc.qkv_norm_rope_bwd(x, Hq, Hk, w, w, rope, None, 1e-6, *g))
+
+    want = []
+    for s in src:
+        torch.cuda.synchronize()
+        out = []
+        for step in range(2):
+            out.append([t.clone() for t in chain(s if step == 0 else s * 0.5)])
+            torch.cuda.synchronize()
+        want.append(out)
+    other = torch.cuda.Stream()
+
+    def both(x):
+        qkv.copy_(x)
+        torch.mul(qkv, 0.5, out=half)
+        other.wait_stream(torch.cuda.current_stream())
+        a = chain(qkv)
+        with torch.cuda.stream(other):
+            b = chain(half)
+        torch.cuda.current_stream().wait_stream(other)
+        joined = moc.window_attention_fwd(a[2], b[3], b[4], *args)  # from both streams' last kernels
+        qkv.zero_()
+        half.zero_()
+        return (*a, *b, *joined)
+
+    joined = []
+    for i, x in enumerate(src):
+        (dq, dk, dv) = want[i][0][2], want[i][1][3], want[i][1][4]
+        joined.append([t.clone() for t in moc.window_attention_fwd(dq, dk, dv, *args)])
+    torch.cuda.synchronize()
+
+    def check(got, i):
+        torch.cuda.synchronize()
+        for x, y in zip(got, (*want[i][0], *want[i][1], *joined[i])):
+            assert torch.equal(x, y)
+
+    for r in range(6):
+        check(both(src[r & 1]), r & 1)
+    x = src[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both(x)
+    for r in range(6):
+        x.copy_(src[r & 1])
+        for t in held:
+            t.zero_()
+        graph.replay()
+        if r % 3 == 2:
+            graph.replay()  # one right after the other
+        check(held, r & 1)
+    moc.check_window_error()
