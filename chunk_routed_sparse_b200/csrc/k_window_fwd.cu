@@ -8,6 +8,8 @@
 // One persistent CTA per SM walks work items (up to 256 consecutive rows of a head, two
 // 128-row tiles A and B that share one key stream) in a fixed order: no counter in
 // memory, so calls on different streams and captured graphs share nothing.
+// (Items handed out by the hardware, clusterlaunchcontrol.try_cancel: 43 -> 45 us on the
+// odd padded batch, 658 -> 715 us on the clip below.)
 //   warp 8 (one lane): TMA of Q tiles and of 128-key K and V tiles (2-stage rings).
 //   warp 9 (one lane): S_q = Q K^T and O_q += P V (P from TMEM), alternating A and
 //          B; an item's last PV and the next item's first S are issued back to back.
