@@ -564,9 +564,11 @@ cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void
     // clip's 1,572 items: 661 against 788 us); up to three items for two SMs the one-tile
     // kernel's shorter chain and finer items end sooner (2,112 tokens, window 256 + 64, d = 64:
     // 18 items 14.9 -> 11.8 us, 81 items 18.5 -> 13.7, 162 items 27.1 -> 20.6, 216 items
-    // 35.4 -> 27.9; open and causal, 33 to 34 us: 108 items -> 22.8, 216 items -> 37.4; at 360
-    // and 408 items the two are level or this one ahead by up to 18 %).
-    if (n_items <= sms + sms / 2) return launch_window_tile(a, d, Q, K, V, O, lse, s);
+    // 35.4 -> 27.9; open and causal, 33 to 34 us: 108 items -> 22.8, 216 items -> 37.4; at 408
+    // items the two are level). Padded batches go there whatever their size, as it hands
+    // items out by demand (24 heads, three sequences, the last empty, up to 9,000 rows: 1.0 to
+    // 1.75 times as fast; one whose rows are all alike loses what the clip loses).
+    if (a.q_len || n_items <= sms + sms / 2) return launch_window_tile(a, d, Q, K, V, O, lse, s);
     return d == 128 ? launch_d<128>(a, n_items, sms, Q, K, V, O, lse, s)
                     : launch_d<64>(a, n_items, sms, Q, K, V, O, lse, s);
 }

@@ -1,7 +1,8 @@
 // Sliding-window attention with always-visible first keys, forward, one 128-row tile
 // per work item: for problems with few row tiles, where each item's chain of product,
-// softmax and product sets the time (k_window_fwd.cu: two tiles an item, which share
-// their keys and hide one another's chain).
+// softmax and product sets the time, and for padded batches, whose items are handed out
+// as CTAs become free (k_window_fwd.cu: two tiles an item, which share their keys and hide
+// one another's chain).
 //
 // The same mathematics, masking, rounding and bounds as there. Here both softmax
 // warpgroups work on the one tile, half of a key tile's columns each (one thread a row
@@ -56,13 +57,13 @@ __device__ __forceinline__ uint32_t p_col(int kk) { return 64u * uint32_t(kk >> 
 
 enum {
     B_Q_FULL = 0, B_Q_EMPTY = 1, B_K_FULL = 2, B_K_EMPTY = 5, B_V_FULL = 8, B_V_EMPTY = 10, B_S_FULL = 12, B_P_FULL = 14,
-    B_PV_DONE = 16, B_EX = 17, B_MMA_DONE = 18, B_COUNT = 19
+    B_PV_DONE = 16, B_EX = 17, B_MMA_DONE = 18, B_ITEM_FULL = 19, B_ITEM_EMPTY = 21, B_COUNT = 23
 };
-struct Shared {
+struct Shared {  // at oBar + 240, after two answers of 16 bytes and the barriers
     uint32_t tmem_base;
     int abort;
 };
-static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
+static_assert(32 + B_COUNT * 8 <= 240, "barriers");
 
 struct Item {
     int b, hq, t0, rows;  // live rows (<= 0: none)
@@ -83,13 +84,15 @@ __device__ __forceinline__ void decode(const WinArgs& a, int nqt, int item, Item
     if (x.rows > 0) x.y = win::span(a, x.seq, x.t0, x.t0 + x.rows);
     x.tiles = x.y.na + x.y.nb;
 }
-// The k-th item of a CTA: rounds over the grid, every other one backwards.
-__device__ __forceinline__ int nth_item(int k) {
+// The n-th item of a CTA: rounds over the grid, every other one backwards.
+__device__ __forceinline__ int nth_item(int n) {
     const int g = int(gridDim.x), i = int(blockIdx.x);
-    return k * g + ((k & 1) ? g - 1 - i : i);
+    return n * g + ((n & 1) ? g - 1 - i : i);
 }
 
-template <int D>
+// Ask: the grid has a CTA for every item, and a running one asks for those that are not
+// launched yet; otherwise it has a CTA an SM, and its items are those of nth_item.
+template <int D, bool Ask>
 __global__ void __launch_bounds__(kThreads, 1)
     window_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WinArgs a, int n_items, int nqt,
@@ -102,15 +105,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) set_error(hdr, ERR_CHECK, 310);
         return;
     }
-    const uint32_t sQ = base + C::oQ, sK = base + C::oK, sV = base + C::oV, sBar = base + C::oBar;
-    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + C::oBar + 8 * B_COUNT);
+    const uint32_t sQ = base + C::oQ, sK = base + C::oK, sV = base + C::oV, sBar = base + C::oBar + 32;
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + C::oBar + 240);
     volatile int* abort = &sh.abort;
     auto bar = [&](int i) { return sBar + 8u * uint32_t(i); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     let_next_kernel_start();
 
     if (tid == 0) {
-        for (int x = 0; x < B_COUNT; ++x) mbar_init(bar(x), (x == B_P_FULL || x == B_P_FULL + 1 || x == B_EX) ? 256 : 1);
+        for (int x = 0; x < B_COUNT; ++x) {
+            int n = x == B_P_FULL || x == B_P_FULL + 1 || x == B_EX ? 256 : 1;
+            if (x >= B_ITEM_EMPTY) n = 2 + 256;  // the loading lane, the issuing one, the softmax warps
+            mbar_init(bar(x), n);
+        }
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -123,7 +130,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(sh.tmem_base)));
     wait_for_previous_kernel();
-    const int n_rounds = (n_items + int(gridDim.x) - 1) / int(gridDim.x);
+    // Ask: item n > 0 of a CTA is its n-th answer, in slot n & 1, the slot's ((n - 1) / 2)-th.
+    auto answer = [&](int n) { return base + C::oBar + 16u * uint32_t(n & 1); };
+    auto full = [&](int n) { return bar(B_ITEM_FULL + (n & 1)); };
+    auto parity = [](int n) { return uint32_t((n - 1) >> 1) & 1u; };
 
     if (warp >= 8) {
         regs_dec<kRegsOther>();
@@ -134,9 +144,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tmV);
             uint32_t g = 0, nq = 0;
             bool stop = false;
-            for (int k = 0; k < n_rounds && !stop; ++k) {
-                const int item = nth_item(k);
-                if (item >= n_items) continue;
+            int asked = 0;  // the answer that is outstanding
+            for (int n = 0, item = int(blockIdx.x); !stop; ++n) {
+                if (!Ask && n > 0) {
+                    item = nth_item(n);
+                    if (item >= n_items) break;
+                } else if (n > 0) {
+                    // asked for once this CTA's last loads are under way: an item claimed earlier
+                    // would wait here while other CTAs have nothing left to do
+                    if (!wait_bar(bar(B_ITEM_EMPTY + (n & 1)), parity(n) ^ 1, abort, hdr, 318)) break;
+                    mbar_expect_tx(full(n), 16);
+                    ask_for_cta(answer(n), full(n));
+                    asked = n;
+                    if (!wait_bar(full(n), parity(n), abort, hdr, 317)) break;
+                    asked = 0;
+                    item = asked_cta(answer(n));
+                    fence_proxy_async_smem();  // read before the slot's next answer
+                    mbar_arrive(bar(B_ITEM_EMPTY + (n & 1)));
+                    if (item < 0) break;
+                }
                 Item x;
                 decode(a, nqt, item, x);
                 if (x.tiles == 0) continue;
@@ -163,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_2d(sV + vs * C::kTileBytes + s * C::kSlabBytes, &tmV, bar(B_V_FULL + vs), 64 * s, krow + key0);
                 }
             }
+            if (asked) drain_bar(full(asked), parity(asked), hdr, 319);
             // every issued copy lands before the CTA exits (after an abort the last V copy may
             // not have been issued: its wait then runs out)
             if (nq > 0) drain_bar(bar(B_Q_FULL), (nq - 1) & 1, hdr, 314);
@@ -191,9 +218,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 return true;
             };
-            for (int k = 0; k < n_rounds && !stop; ++k) {
-                const int item = nth_item(k);
-                if (item >= n_items) continue;
+            for (int n = 0, item = int(blockIdx.x); !stop; ++n) {
+                if (!Ask && n > 0) {
+                    item = nth_item(n);
+                    if (item >= n_items) break;
+                } else if (n > 0) {
+                    if (!wait_bar_warp(full(n), parity(n), abort, hdr, 326)) break;
+                    item = uniform(asked_cta(answer(n)));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (leader) mbar_arrive(bar(B_ITEM_EMPTY + (n & 1)));
+                    __syncwarp();
+                    if (item < 0) break;
+                }
                 Item x;
                 decode(a, nqt, item, x);
                 const int T = uniform(x.tiles);
@@ -247,9 +284,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         bool stop = false;
-        for (int k = 0; k < n_rounds && !stop; ++k) {
-            const int item = nth_item(k);
-            if (item >= n_items) continue;
+        for (int n = 0, item = int(blockIdx.x); !stop; ++n) {
+            if (!Ask && n > 0) {
+                item = nth_item(n);
+                if (item >= n_items) break;
+            } else if (n > 0) {
+                if (!wait_bar_warp(full(n), parity(n), abort, hdr, 336)) break;
+                item = asked_cta(answer(n));
+                fence_proxy_async_smem();
+                mbar_arrive(bar(B_ITEM_EMPTY + (n & 1)));
+                if (item < 0) break;
+            }
             Item x;
             decode(a, nqt, item, x);
             // rows to write: the live ones, and with a.fill those past the last
@@ -409,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool Ask>
 cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void* V, void* O, float* lse,
                      cudaStream_t s) {
     int32_t* hdr = nullptr;
@@ -421,21 +466,27 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     if (krows == 0) tmK = tmV = tmQ;  // no key tile is loaded
     else if (!make_tmap(&tmK, K, D, krows) || !make_tmap(&tmV, V, D, krows)) return cudaErrorInvalidValue;
     const int smem = Cfg<D>::kSmem;
-    e = cudaFuncSetAttribute(window_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(window_tile_kernel<D, Ask>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    const int nqt = (a.Lq + 127) / 128, n_items = a.B * a.Hq * nqt;
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int nqt = (a.Lq + 127) / 128, n_items = a.B * a.Hq * nqt;
-    return launch_after(window_tile_kernel<D>, n_items < sms ? n_items : sms, kThreads, smem, s, tmQ, tmK, tmV,
-                        a, n_items, nqt, hdr, static_cast<__nv_bfloat16*>(O), lse);
+    return launch_after(window_tile_kernel<D, Ask>, !Ask && n_items > sms ? sms : n_items, kThreads, smem, s, tmQ, tmK,
+                        tmV, a, n_items, nqt, hdr, static_cast<__nv_bfloat16*>(O), lse);
 }
 
 }  // namespace
 
 cudaError_t launch_window_tile(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
                                float* lse, cudaStream_t s) {
-    return d == 128 ? launch_d<128>(a, Q, K, V, O, lse, s) : launch_d<64>(a, Q, K, V, O, lse, s);
+    // Items of equal rows go in rounds: asking costs them up to 13 % (18 heads of 2,112 rows,
+    // 256 keys either side: 19.8 against 22.4 us). In a padded batch rounds leave some CTAs
+    // the items without rows: three sequences, the last empty, 12 heads, 700 keys back, open
+    // and causal at 2,501 rows 43.6 and 57.6 us in rounds, 31.9 and 37.1 asking.
+    if (a.q_len)
+        return d == 128 ? launch_d<128, true>(a, Q, K, V, O, lse, s) : launch_d<64, true>(a, Q, K, V, O, lse, s);
+    return d == 128 ? launch_d<128, false>(a, Q, K, V, O, lse, s) : launch_d<64, false>(a, Q, K, V, O, lse, s);
 }
 
 }  // namespace moc

@@ -237,6 +237,31 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Asks the hardware for a CTA of this grid that has not been launched, to do its work
+// here: 16 bytes to dst and their count to the mbarrier. After an answer without one, no
+// more may be asked.
+__device__ __forceinline__ void ask_for_cta(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer's blockIdx.x, or -1.
+__device__ __forceinline__ int asked_cta(uint32_t src) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b64 lo, hi;\n\t"
+        "ld.shared.v2.b64 {lo, hi}, [%2];\n\t"
+        "mov.b128 h, {lo, hi};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return ok ? int(x) : -1;
+}
+
 // One lane of a converged warp (the same one each time).
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;

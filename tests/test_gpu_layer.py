@@ -155,6 +155,42 @@ def test_calls_on_two_streams_at_once():
             assert torch.equal(x, y)
 
 
+def test_padded_batches_on_two_streams_and_in_a_graph():
+    """Their row tiles go to CTAs as these become free: in another order every time, with
+    the same bits, next to another call or replayed."""
+    L = [2501, 1900]
+    lens = [torch.tensor(x, device="cuda", dtype=torch.int32) for x in ([2501, 0, 1311], [3, 1900, 1024, 127])]
+    t = [[_rand(len(n), 12, l, 64, seed=70 + 4 * i + j) for j in range(4)] for i, (n, l) in enumerate(zip(lens, L))]
+    args = [(700, 0, 5, True), (64, 64, 300, False)]
+
+    def step(i):
+        q, k, v, g = t[i]
+        o, lse = moc.window_attention_fwd(q, k, v, *args[i], lens[i], lens[i])
+        return (o, lse, *moc.window_attention_bwd(q, k, v, o, lse, g, *args[i], lens[i], lens[i]))
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append((i, step(i)))
+    torch.cuda.synchronize()
+    for i, g in got:
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(0)
+    for _ in range(3):
+        for x in held:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(held, want[0]))
+    moc.check_window_error()
+
+
 def test_two_graphs_that_share_a_workspace():
     Q, K, V, g = (_rand(1, 4, 2000, 64, seed=50 + i) for i in range(4))
     cases = [(300, 0, 140, True), (40, 0, 7, True)]
