@@ -364,8 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item x;
             decode(a, item, x);
             const QTile qt = tile_of(a, x, q);
-            // rows to write: the live ones, and with a.fill those past the last
-            const int rows_out = a.fill ? min(128, a.Lq - x.t0 - 128 * q) : qt.rows;
+            const int rows_out = qt.rows;  // all rows live: padded batches take the one-tile kernel
             if (rows_out <= 0) {
                 gt += x.tiles;
                 continue;
