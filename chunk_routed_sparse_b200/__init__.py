@@ -15,6 +15,13 @@ Pipeline (pages: "Mixture of Contexts for Long Video Generation | Summary"
     O, lse = attention_fwd(layout, Q, K, V, sel, k)  # (3) lists, (4) attend, (5) merge
 
 Q, K, V are bf16 CUDA tensors [B, H, L, d] (head-major, contiguous), d in {64, 128}.
+
+Around it (``rows.py``, ``window.py``): rotary positions, the norm and rotation of a
+packed projection into such Q, K, V, and an attention with a sliding window and
+always-visible first keys; all differentiable.
+
+    Q, K, V = qkv_norm_rope(qkv, Hq, Hk, wq, wk, Rope(128, axes=(44, 42, 42)), pos)
+    O = window_attention(Q, K, V, left=1560, right=1560, sinks=512)
 """
 from __future__ import annotations
 
