@@ -20,6 +20,16 @@ __device__ __forceinline__ uint4 ldg_nc16(const void* p) {
     return v;
 }
 
+// The same load of data that may be written while the kernel is resident (by the kernel
+// before it in the stream, or by this one): ld.global.nc is defined for memory that is
+// read-only for the kernel's whole life alone.
+__device__ __forceinline__ void ld16(const void* p, uint32_t* w) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

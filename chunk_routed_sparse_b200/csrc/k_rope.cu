@@ -43,17 +43,9 @@ struct Raw {
     uint32_t w[kWords];
 };
 
-__device__ __forceinline__ void ld16(const void* p, uint32_t* w) {
-    // plain (not read-only) path: the output may be the input itself
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p)
-                 : "memory");
-}
-
 template <typename T, bool AL>
 __device__ __forceinline__ void load_raw(const T* p, Raw<T>& r) {
-    if constexpr (AL) {
+    if constexpr (AL) {  // (not the read-only path: the output may be the input itself)
 #pragma unroll
         for (int i = 0; i < Raw<T>::kWords; i += 4) ld16(reinterpret_cast<const uint32_t*>(p) + i, r.w + i);
     } else if constexpr (sizeof(T) == 4) {

@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
         float acc = 0.f, l2 = -INFINITY;
         if (head < heads && t < win::seq(a, int(head / a.Hq)).m) {
             const size_t row = size_t(head) * a.Lq + t;
-            const uint4 x = ldg_nc16(O + row * D + r * 8), y = ldg_nc16(dO + row * D + r * 8);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            uint32_t xs[4], ys[4];
+            ld16(O + row * D + r * 8, xs);
+            ld16(dO + row * D + r * 8, ys);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 acc = fmaf(bf16lo(xs[k]), bf16lo(ys[k]), acc);

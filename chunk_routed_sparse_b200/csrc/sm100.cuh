@@ -221,7 +221,8 @@ __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepc
 // kernel before it in the stream end: launch latency and set-up pass under that kernel's
 // tail (window attention of the odd padded batch and its gradient, five kernels: 140.4 ->
 // 132.7 us). What another kernel of the stream wrote is read with ordinary loads or
-// copies (a load through const __restrict__ may be moved ahead of the wait).
+// copies: a load through const __restrict__ may be moved ahead of the wait, and ld.global.nc
+// wants memory that nothing writes while the kernel is resident.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
