@@ -27,6 +27,8 @@
 // dQ kernel adds the sum r of its unrounded ds to D for the dK / dV kernel, and walks
 // units of at most kProbeKeys keys twice, the first time for r alone (two of their
 // three products again; such units are short).
+#include <type_traits>
+
 #include "common.cuh"
 #include "pipeline.cuh"
 #include "tmap.cuh"
@@ -51,6 +53,13 @@ constexpr int kFineRows = 64;
 // What two bf16 of a packed pair leave of (x, y), as bf16.
 __device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t pk) {
     return pack_bf16(x - bf16lo(pk), y - bf16hi(pk));
+}
+
+// Halves of a packed pair to keep: the low one for bit i of `bits`, the high one for bit i + 1.
+__device__ __forceinline__ uint32_t pair_mask(uint32_t bits, int i) {
+    uint32_t m;  // bytes 3 of the shifted words, their sign over 16 bits each
+    asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(m) : "r"(bits << (31 - i)), "r"(bits << (30 - i)));
+    return m;
 }
 
 // Row statistics, negated for the sums they enter: - log2 sum exp2 of the scores and
@@ -1000,33 +1009,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!wait_bar_warp(bar(B_DP_FULL), g & 1, abort, hdr, 285)) { stop = true; break; }
                 tc_fence_after();
-                if (n < kTile) {  // dP^T of a row past the last may be NaN
-#pragma unroll 1
-                    for (int w = 0; w < 2; ++w) mask_cols(g_addr + 32 * w, win::bits(0, n - 64 * wg - 32 * w), 0u);
-                    tmem_wait_st();
-                }
+                // ds is zero where the row does not see the key: p is zero there, but dP or D of a
+                // value, a gradient or a row past the last that nobody sees may be NaN. (A body
+                // of its own for the edge tiles: 8,000 rows, window 256 + 256, 198.5 -> 201.3 us a
+                // gradient; in one body for all tiles 202.4, and the long causal step 1 % slower.)
+                auto form_ds = [&](auto edge) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t d[32], pk[16], rest[Fine ? 16 : 1];
-                    tmem_ld32(g_addr + 32 * c, d);
-                    tmem_wait_ld_regs(d);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t d[32], pk[16], rest[Fine ? 16 : 1];
+                        tmem_ld32(g_addr + 32 * c, d);
+                        tmem_wait_ld_regs(d);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float4 q = *reinterpret_cast<const float4*>(stat + 128 + 32 * c + 2 * e);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 q = *reinterpret_cast<const float4*>(stat + 128 + 32 * c + 2 * e);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int i0 = 2 * (e + h);
-                            float d0, d1;
-                            f2_unpack(f2_mul(f2_pack(__uint_as_float(s[32 * c + i0]), __uint_as_float(s[32 * c + i0 + 1])),
-                                             f2_add(f2_pack(__uint_as_float(d[i0]), __uint_as_float(d[i0 + 1])),
-                                                    h == 0 ? f2_pack(q.x, q.y) : f2_pack(q.z, q.w))), d0, d1);
-                            pk[e + h] = pack_bf16(d0, d1);
-                            if constexpr (Fine) rest[e + h] = pack_rest(d0, d1, pk[e + h]);
+                            for (int h = 0; h < 2; ++h) {
+                                const int i0 = 2 * (e + h);
+                                float d0, d1;
+                                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[32 * c + i0]), __uint_as_float(s[32 * c + i0 + 1])),
+                                                 f2_add(f2_pack(__uint_as_float(d[i0]), __uint_as_float(d[i0 + 1])),
+                                                        h == 0 ? f2_pack(q.x, q.y) : f2_pack(q.z, q.w))), d0, d1);
+                                pk[e + h] = pack_bf16(d0, d1);
+                                if constexpr (Fine) rest[e + h] = pack_rest(d0, d1, pk[e + h]);
+                            }
                         }
+                        if constexpr (decltype(edge)::value) {
+                            const uint32_t see = win::bits(lo - 32 * c, hi - 32 * c);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint32_t keep = pair_mask(see, 2 * e);
+                                pk[e] &= keep;
+                                if constexpr (Fine) rest[e] &= keep;
+                            }
+                        }
+                        tmem_st16(g_addr + (Fine ? 32 : 16) * c, pk);
+                        if constexpr (Fine) tmem_st16(g_addr + 32 * c + 16, rest);
                     }
-                    tmem_st16(g_addr + (Fine ? 32 : 16) * c, pk);
-                    if constexpr (Fine) tmem_st16(g_addr + 32 * c + 16, rest);
-                }
+                };
+                if (masked) form_ds(std::true_type{});
+                else form_ds(std::false_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(B_DS_FULL));
