@@ -610,7 +610,8 @@ static_assert(B_COUNT * 8 + sizeof(Shared) <= 256, "barriers");
 // A unit: a key tile of a (batch, key head), all of its row tiles or one split of them.
 struct Unit {
     int b, hk, k0, nk;     // nk <= 0: no keys
-    int t_lo, t_hi;        // rows of a query head that may see it
+    int t_lo, t_hi;        // rows of a query head that may see it, from a multiple of four
+    int skip;              // rows at t_lo that come before the first that does
     int per_head;          // their tiles
     int i0, i1;            // this unit's tiles, counted over the heads of the group
     int part;              // split: index of the fp32 part, else -1
@@ -635,13 +636,15 @@ __device__ __forceinline__ void decode(const WinArgs& a, const WinBwdPlan& p, in
     x.k0 = kt * kTile;
     x.seq = win::seq(a, x.b);
     x.nk = min(kTile, x.seq.n - x.k0);
-    x.t_lo = x.t_hi = x.per_head = x.i0 = x.i1 = 0;
+    x.t_lo = x.t_hi = x.skip = x.per_head = x.i0 = x.i1 = 0;
     if (x.nk <= 0) return;
     const bool first = x.k0 < a.sinks;
     int p_lo = first ? -(1 << 30) : x.k0 - a.right;
     if (a.causal) p_lo = max(p_lo, x.k0);
     const int p_hi = first ? (1 << 30) : x.k0 + x.nk - 1 + a.left;  // last position
-    x.t_lo = max(p_lo - x.seq.shift, 0) & ~3;                       // 16-byte copies of the statistics
+    const int t_first = max(p_lo - x.seq.shift, 0);
+    x.t_lo = t_first & ~3;                                          // 16-byte copies of the statistics
+    x.skip = t_first - x.t_lo;
     x.t_hi = min(p_hi - x.seq.shift + 1, x.seq.m);
     if (x.t_hi <= x.t_lo) return;
     x.per_head = (x.t_hi - x.t_lo + kTile - 1) / kTile;
@@ -942,17 +945,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool stop = false;
             RowWalk walk(a, x);
             for (int i = x.i0; i < x.i1; ++i, ++g, walk.next(x)) {
-                const int t0 = walk.t0, n = walk.rows(x);
+                const int t0 = walk.t0, n = walk.rows(x), skip = walk.r == 0 ? x.skip : 0;
                 const uint32_t os = g & 1, s_addr = lane_addr + C::col_st(g) + 64 * wg;
                 // dO and the statistics (their own barrier makes the copies visible here), S^T
                 if (!wait_bar_warp(bar(B_O_FULL + os), (g >> 1) & 1, abort, hdr, 282)) { stop = true; break; }
                 if (!wait_bar_warp(bar(B_S_FULL + (g & 1)), (g >> 1) & 1, abort, hdr, 283)) { stop = true; break; }
                 tc_fence_after();
                 float* stat = reinterpret_cast<float*>(smem_raw + C::oStat + os * C::kStatBytes) + 64 * wg;
-                if (n < kTile) {
-                    // rows past the last: nothing of theirs (whatever was loaded) may reach a
-                    // product. dP^T may still be reading dO: what it makes of these rows is masked.
-                    if (row >= n) {
+                if (n < kTile || skip > 0) {
+                    // rows past the last or before the first: nothing of theirs (whatever was loaded)
+                    // may reach a product. dP^T may still be reading dO: what it makes of these rows
+                    // is masked.
+                    if (row >= n || row < skip) {
                         if ((row >> 6) == wg) {
                             stat[row & 63] = -INFINITY;
                             stat[128 + (row & 63)] = 0.f;

@@ -550,9 +550,13 @@ size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t L
  *   dK_u = scale sum_t ds_tu q_t,      dV_u = sum_t p_tu dO_t,
  * sums in fp32 (over the rows of every query head that reads the key head), each
  * result rounded once. Rows that see no key get dQ = 0, keys that no row sees
- * dK = dV = 0; rows of dQ past q_len and of dK, dV past kv_len are left as they
- * were (fill_rest 0) or set to 0 (1). ws: 256-byte aligned, contents free before and after; two calls that may
- * overlap need two. Deterministic on one device model. */
+ * dK = dV = 0, whatever such rows and keys hold, and they reach no other result;
+ * rows of dQ past q_len and of dK, dV past kv_len are left as they were (fill_rest
+ * 0) or set to 0 (1). (An infinity or a NaN in a key that only some rows of 128
+ * see can reach dQ of the others of them as 0 x infinity, and one in Q or dO of a
+ * row that sees only some keys of 128 dK and dV of the others.) ws: 256-byte
+ * aligned, contents free before and after; two calls that may overlap need two.
+ * Deterministic on one device model. */
 moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                     const void* K, const void* V, const void* O, const float* lse, const void* dO,
                                     int64_t left, int64_t right, int64_t sinks, int causal, const int32_t* q_len,

@@ -59,3 +59,34 @@ def test_keys_that_no_row_sees_reach_nothing(case, bad):
         for name, x, y in zip(("O", "lse", "dQ", "dK", "dV"), got, want):
             assert torch.equal(x, y), (which, name)
         assert (got[3][:, :, unseen] == 0).all() and (got[4][:, :, unseen] == 0).all()
+
+
+ROWS = [  # more rows than keys: the first rows see nothing; the first row that does is no multiple of four
+    (1, 4, 2, 300, 98, 64, 20, 0, 4, True),
+    (1, 4, 2, 300, 99, 128, 20, 0, 4, True),
+    (2, 2, 2, 300, 100, 64, 20, 29, 0, False),
+    (2, 2, 1, 301, 134, 128, 20, 6, 0, False),
+    (1, 3, 1, 40, 5, 128, 90, 0, 3, True),         # gradients of few rows
+    (1, 2, 1, 7, 2, 64, -1, 0, 0, True),           # the few-row kernel
+    (1, 250, 1, 300, 101, 64, 20, 0, 4, True),     # the forward's two-tile kernel
+]
+
+
+@pytest.mark.parametrize("case", ROWS, ids=str)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_rows_that_see_no_key_reach_nothing(case, bad):
+    B, Hq, Hk, Lq, Lk, d, *args = case
+    Q, K, V, g = _rand(B, Hq, Lq, d, seed=1), _rand(B, Hk, Lk, d, seed=2), _rand(B, Hk, Lk, d, seed=3), _rand(B, Hq, Lq, d, seed=4)
+    want = _step(Q, K, V, g, args)
+    blind = ~W.visible(Lk, Lq, *args).any(1).cuda()
+    assert blind.any() and not blind.all()
+    for which in ("Q", "dO", "Q dO"):
+        q, u = Q.clone(), g.clone()
+        if "Q" in which:
+            q[:, :, blind] = bad
+        if "dO" in which:
+            u[:, :, blind] = bad
+        got = _step(q, K, V, u, args)
+        for name, x, y in zip(("O", "lse", "dQ", "dK", "dV"), got, want):
+            assert torch.equal(x, y), (which, name)
+        assert (got[0][:, :, blind] == 0).all() and (got[2][:, :, blind] == 0).all()
