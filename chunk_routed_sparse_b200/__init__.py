@@ -59,7 +59,7 @@ _lib = None
 
 # name -> (restype, argtypes); every symbol include/moc.h declares
 _I, _I64, _P, _F, _SZ = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
-_WIN = [_I64, _I64, _I64, _I, _P, _P, _I, _F]  # left, right, sinks, causal, q_len, kv_len, fill_rest, scale
+_WIN = [_I64, _I64, _I64, _I, _P, _P, _I, _F]  # left, right, sinks, causal, q_len, kv_len, fill_rest or flags, scale
 _POS = [_P, _I64, _I64]  # positions: pointer, batch stride, axis stride
 SIGNATURES = {
     "moc_status_string": (ctypes.c_char_p, [_I]),

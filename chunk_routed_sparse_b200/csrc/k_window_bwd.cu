@@ -26,7 +26,8 @@
 // feels as much as the roundings of p and ds. As sum_u ds_tu = 0 for the exact D, the
 // dQ kernel adds the sum r of its unrounded ds to D for the dK / dV kernel, and walks
 // units of at most kProbeKeys keys twice, the first time for r alone (two of their
-// three products again; such units are short).
+// three products again; such units are short). That holds where O and lse are those of
+// exactly this call's keys: with a.joined they are not, and D is dO . O.
 #include <type_traits>
 
 #include "common.cuh"
@@ -189,7 +190,7 @@ __device__ __forceinline__ void decode(const WinArgs& a, int nqt, int u, Unit& x
     x.y = win::Span{0, 0, 0, 0, 0};
     if (x.rows > 0) x.y = win::span(a, x.seq, x.t0, x.t0 + x.rows);
     x.tiles = x.y.na + x.y.nb;
-    x.probe = x.y.a1 + x.y.b1 - x.y.b0 <= kProbeKeys ? x.tiles : 0;
+    x.probe = !a.joined && x.y.a1 + x.y.b1 - x.y.b0 <= kProbeKeys ? x.tiles : 0;
 }
 
 template <int D, bool Fine>
@@ -508,8 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (stop) break;
             // dq_t = scale * accumulator; this warpgroup's half of the columns
             if (x.tiles > 0) {
-                if (!add_both(half_sum())) break;
-                if (wg == 0 && live && l2 != -INFINITY) nd[srow] = drow;
+                if (!a.joined) {
+                    if (!add_both(half_sum())) break;
+                    if (wg == 0 && live && l2 != -INFINITY) nd[srow] = drow;
+                }
                 if (!wait_bar_warp(bar(B_DQ_DONE), nu & 1, abort, hdr, 254)) break;
                 ++nu;
                 tc_fence_after();

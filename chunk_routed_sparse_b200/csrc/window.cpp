@@ -76,13 +76,15 @@ extern "C" size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk
 extern "C" moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                                const void* K, const void* V, const void* O, const float* lse,
                                                const void* dO, int64_t left, int64_t right, int64_t sinks, int causal,
-                                               const int32_t* q_len, const int32_t* kv_len, int fill_rest,
+                                               const int32_t* q_len, const int32_t* kv_len, int flags,
                                                float softmax_scale, void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
                                                moc_stream_t stream) {
+    if (flags & ~(MOC_WINDOW_FILL_REST | MOC_WINDOW_JOINED)) return MOC_ERR_INVALID_ARG;
     moc::WinArgs a{};
-    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len, fill_rest,
-                                    softmax_scale);
+    const moc_status st = make_args(a, B, Hq, Hk, Lq, Lk, d, left, right, sinks, causal, q_len, kv_len,
+                                    flags & MOC_WINDOW_FILL_REST, softmax_scale);
     if (st != MOC_OK) return st;
+    a.joined = flags & MOC_WINDOW_JOINED ? 1 : 0;
     if (B == 0 || Hq == 0 || (Lq == 0 && Lk == 0)) return MOC_OK;
     if (Lq > 0)
         for (const void* t : {Q, O, dO, static_cast<const void*>(dQ)})

@@ -27,6 +27,7 @@ struct WinArgs {
     const int32_t* kv_len;      // [B] or null: Lk
     float scale;
     int32_t fill;               // rows past the lengths: 0 left as they were, 1 written as empty
+    int32_t joined;             // backward: O and lse go over more keys than this call's
 };
 
 #ifdef __CUDACC__

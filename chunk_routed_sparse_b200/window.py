@@ -25,6 +25,7 @@ from .rows import _at, _call, _workspace_bytes
 
 
 _FAR = 1 << 40
+_FILL_REST, _JOINED = 1, 2  # MOC_WINDOW_FILL_REST, MOC_WINDOW_JOINED
 
 
 def _tensor(name, x, shape, device, dtype=torch.bfloat16):
@@ -91,9 +92,13 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
                          q_len: Optional[torch.Tensor] = None, kv_len: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, dQ: Optional[torch.Tensor] = None,
                          dK: Optional[torch.Tensor] = None, dV: Optional[torch.Tensor] = None,
-                         ws: Optional[torch.Tensor] = None):
+                         ws: Optional[torch.Tensor] = None, joined: bool = False):
     """(dQ, dK, dV) for the upstream gradient dO (moc_window_attention_bwd). Rows past
-    the lengths are left as they were in given tensors and are 0 in new ones."""
+    the lengths are left as they were in given tensors and are 0 in new ones.
+
+    O and lse are window_attention_fwd's for the same arguments; with ``joined`` those of
+    a softmax over more keys than this call's (O and lse joined over several key ranges,
+    one call a range, whose dQ add up)."""
     B, Hq, Hk, Lq, Lk, d = _problem(Q, K, V, q_len, kv_len)
     left, right, sinks = _limits(left, right, sinks)
     _tensor("O", O, Q.shape, Q.device)
@@ -115,7 +120,8 @@ def window_attention_bwd(Q, K, V, O, lse, dO, left: int = -1, right: int = -1, s
         raise ValueError(f"ws: expected a contiguous tensor on {Q.device}")
     _call("moc_window_attention_bwd", Q.device, B, Hq, Hk, Lq, Lk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
           O.data_ptr(), lse.data_ptr(), dO.data_ptr(), left, right, sinks, 1 if causal else 0, _at(q_len), _at(kv_len),
-          fill, scale, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+          (_FILL_REST if fill else 0) | (_JOINED if joined else 0), scale, dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+          ws.data_ptr(), ws.numel() * ws.element_size())
     return dQ, dK, dV
 
 

@@ -543,16 +543,25 @@ moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, i
 size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, int64_t left,
                                                 int64_t right, int64_t sinks, int causal);
 
+/* Flags of moc_window_attention_bwd. */
+enum { MOC_WINDOW_FILL_REST = 1, MOC_WINDOW_JOINED = 2 };
+
 /* Gradient of moc_window_attention: dQ, dK, dV (bf16, contiguous as Q, K, V) for an
- * upstream gradient dO of O, from the forward pass's O and lse. With
- * p_tu = exp(scale q_t . k_u - lse_t) over the visible keys and D_t = dO_t . O_t:
+ * upstream gradient dO of O. With p_tu = exp(scale q_t . k_u - lse_t) over the
+ * visible keys and D_t = dO_t . O_t:
  *   ds_tu = p_tu (dO_t . v_u - D_t),   dQ_t = scale sum_u ds_tu k_u,
  *   dK_u = scale sum_t ds_tu q_t,      dV_u = sum_t p_tu dO_t,
  * sums in fp32 (over the rows of every query head that reads the key head), each
- * result rounded once. Rows that see no key get dQ = 0, keys that no row sees
+ * result rounded once. O and lse are those that moc_window_attention gave for the
+ * same Q, K, V, window and lengths: sum_u ds_tu is then zero, and what the rounding
+ * of O puts into D is taken out by that (dK always, dQ where a row's keys are few).
+ * With MOC_WINDOW_JOINED in flags they are those of a softmax over more keys, of
+ * which this call has a part (O and lse joined over several key ranges, one gradient
+ * call a range: the ranges' dQ add up, dK and dV are each range's own), and D is
+ * dO . O as given. Rows that see no key get dQ = 0, keys that no row sees
  * dK = dV = 0, whatever such rows and keys hold, and they reach no other result;
- * rows of dQ past q_len and of dK, dV past kv_len are left as they were (fill_rest
- * 0) or set to 0 (1). (An infinity or a NaN in a key that only some rows of 128
+ * rows of dQ past q_len and of dK, dV past kv_len are left as they were, or set to 0
+ * with MOC_WINDOW_FILL_REST in flags. (An infinity or a NaN in a key that only some rows of 128
  * see can reach dQ of the others of them as 0 x infinity, and one in Q or dO of a
  * row that sees only some keys of 128 dK and dV of the others.) ws: 256-byte
  * aligned, contents free before and after; two calls that may overlap need two.
@@ -560,7 +569,7 @@ size_t moc_window_attention_bwd_workspace_bytes(int B, int Hq, int Hk, int64_t L
 moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                     const void* K, const void* V, const void* O, const float* lse, const void* dO,
                                     int64_t left, int64_t right, int64_t sinks, int causal, const int32_t* q_len,
-                                    const int32_t* kv_len, int fill_rest, float softmax_scale, void* dQ, void* dK,
+                                    const int32_t* kv_len, int flags, float softmax_scale, void* dQ, void* dK,
                                     void* dV, void* ws, size_t ws_bytes, moc_stream_t stream);
 
 /* Read and clear the current device's error word of the window calls, as
