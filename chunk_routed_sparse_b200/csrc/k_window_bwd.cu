@@ -1225,7 +1225,7 @@ WinBwdPlan plan_window_bwd(const WinArgs& a, int d) {
     const int64_t heads = int64_t(a.B) * a.Hk;
     if (p.split_tiles > 0 && heads > 0 && a.Lq > 0) {
         const int64_t all = (a.Lq + kTile - 1) / kTile;
-        const int64_t reach = (a.left == kWinOpen ? a.Lq : a.left) + (a.causal ? 0 : a.right == kWinOpen ? a.Lq : a.right);
+        const int64_t reach = (a.left == kWinOpen ? a.Lq : a.left) + (a.right == kWinOpen ? a.Lq : a.right);
         const int64_t near = (reach + kTile - 1) / kTile + 1;
         int64_t n = (all + near - 1) / near;
         const int64_t cap = (4 * int64_t(sm_count()) + p.split_tiles * heads - 1) / (p.split_tiles * heads);

@@ -339,7 +339,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     const int64_t heads = int64_t(a.B) * a.Hk;
     const int64_t keys = a.left == kWinOpen || a.right == kWinOpen
                              ? a.Lk
-                             : int64_t(a.left) + (a.causal ? 0 : a.right) + a.Lq + a.sinks;
+                             : int64_t(a.left) + a.right + a.Lq + a.sinks;
     const int64_t tiles = ((keys < a.Lk ? keys : a.Lk) + kKeys - 1) / kKeys;
     int cs = 1;
     while (cs < kMaxCluster && heads * cs < 4 * int64_t(sms) && tiles >= 4 * cs) cs *= 2;

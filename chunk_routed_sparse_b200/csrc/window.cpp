@@ -32,7 +32,9 @@ moc_status make_args(moc::WinArgs& a, int B, int Hq, int Hk, int64_t Lq, int64_t
     a.Lk = int32_t(Lk);
     // a limit that reaches every key from every row is none
     a.left = left < 0 || left >= Lq + Lk ? moc::kWinOpen : int32_t(left);
-    a.right = right < 0 || right >= Lq + Lk ? moc::kWinOpen : int32_t(right);
+    // (causal: no key lies right of a row, whatever the limit; said once, so that every estimate
+    // of a row's reach sees it)
+    a.right = causal ? 0 : right < 0 || right >= Lq + Lk ? moc::kWinOpen : int32_t(right);
     a.sinks = int32_t(sinks < Lk ? sinks : Lk);
     a.causal = causal ? 1 : 0;
     a.q_len = q_len;

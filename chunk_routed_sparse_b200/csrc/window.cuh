@@ -21,7 +21,7 @@ constexpr int kWinOpen = 1 << 30;  // left / right: no limit
 struct WinArgs {
     int32_t B, Hq, Hk, group;   // group = Hq / Hk query heads share a key head
     int32_t Lq, Lk;
-    int32_t left, right, sinks; // kWinOpen: no limit (left, right)
+    int32_t left, right, sinks; // kWinOpen: no limit (left, right); causal: right is 0
     int32_t causal;
     const int32_t* q_len;       // [B] or null: Lq
     const int32_t* kv_len;      // [B] or null: Lk
