@@ -58,7 +58,7 @@ def _problem(Q, K, V, q_len, kv_len):
 
 def _limits(left, right, sinks):
     """The window's sizes in 64 bits: any negative limit is none, any huge one reaches every key."""
-    if 0 <= left < _FAR and 0 <= right < _FAR and 0 <= sinks < _FAR:
+    if -1 <= left < _FAR and -1 <= right < _FAR and 0 <= sinks < _FAR:
         return int(left), int(right), int(sinks)
     return tuple(max(min(int(x), _FAR), -1) for x in (left, right, sinks))
 
