@@ -518,13 +518,6 @@ __global__ void __launch_bounds__(1024) rows_dw_kernel(int ctas, int D, const fl
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 // fn<T, D, HALF, AL>(args...) for the runtime type, width, pair layout and alignment
 #define MOC_ROWS_DISPATCH(CALL)                                                     \
     do {                                                                            \
@@ -560,13 +553,13 @@ static dim3 rows_grid(int d, int64_t tokens, int heads, int64_t want, int64_t mo
 }
 
 static dim3 rows_bwd_grid(int d, int64_t tokens, int heads, int* heads_per_cta) {
-    const int64_t n = kBwdCtas * int64_t(sm_count());
+    const int64_t n = kBwdCtas * int64_t(sm100::multiprocessors());
     return rows_grid(d, tokens, heads, n, n, heads_per_cta);
 }
 
 cudaError_t launch_rows_fwd(int dtype, int d, bool aligned, const RowArgs& args, cudaStream_t s) {
     RowArgs a = args;
-    const dim3 grid = rows_grid(d, a.tokens, a.heads, 8 * int64_t(sm_count()), INT64_MAX, &a.heads_per_cta);
+    const dim3 grid = rows_grid(d, a.tokens, a.heads, 8 * int64_t(sm100::multiprocessors()), INT64_MAX, &a.heads_per_cta);
 #define MOC_CALL(T, D, HALF, AL) e = sm100::launch_after(rows_fwd_kernel<T, D, HALF, AL>, grid, kThreads, 0, s, a)
     cudaError_t e = cudaSuccess;
     MOC_ROWS_DISPATCH(MOC_CALL);

@@ -39,6 +39,9 @@ namespace moc {
 namespace {
 
 using namespace sm100;
+using win::kRegsCompute;
+using win::kRegsOther;
+using win::kThreads;
 using win::kTile;
 
 constexpr uint32_t kTmemCols = 512;
@@ -137,9 +140,6 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 //          columns; Fine: what that leaves of it over the other 32).
 namespace dq {
 
-constexpr int kThreads = 384;
-// launched at 168 registers a thread: 2 x 128 x 216 + 128 x 72 = 384 x 168
-constexpr int kRegsCompute = 216, kRegsOther = 72;
 constexpr uint32_t kColS0 = 0, kColS1 = 128, kColDP = 256, kColDQ = 384;
 
 template <int D>
@@ -171,25 +171,11 @@ __device__ __forceinline__ uint32_t col_s(int b) { return b ? kColS1 : kColS0; }
 // column (from a buffer's first) of the bf16 pairs of keys 16 kk .. + 15
 __device__ __forceinline__ uint32_t ds_col(int kk) { return 64u * uint32_t(kk >> 2) + 8u * uint32_t(kk & 3); }
 
-struct Unit {
-    int b, hq, t0, rows;
-    int tiles;  // key tiles
+struct Unit : win::Item {
     int probe;  // tiles walked first for the sum of ds alone: `tiles` or 0
-    win::Seq seq;
-    win::Span y;
 };
-// the last rows (the longest spans under an open causal window) first
 __device__ __forceinline__ void decode(const WinArgs& a, int nqt, int u, Unit& x) {
-    const int heads = a.B * a.Hq;
-    const int qt = nqt - 1 - u / heads, bh = u % heads;
-    x.b = bh / a.Hq;
-    x.hq = bh - x.b * a.Hq;
-    x.t0 = qt * kTile;
-    x.seq = win::seq(a, x.b);
-    x.rows = min(kTile, x.seq.m - x.t0);
-    x.y = win::Span{0, 0, 0, 0, 0};
-    if (x.rows > 0) x.y = win::span(a, x.seq, x.t0, x.t0 + x.rows);
-    x.tiles = x.y.na + x.y.nb;
+    win::decode(a, kTile, nqt, u, x);
     x.probe = !a.joined && x.y.a1 + x.y.b1 - x.y.b0 <= kProbeKeys ? x.tiles : 0;
 }
 
@@ -571,10 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   warps 0-7: two warpgroups, each 64 of the tile's rows for all 128 keys (one thread
 //          a key): P^T, then dS^T, as bf16 over its own halves of S^T and dP^T.
 namespace dkv {
-
-constexpr int kThreads = 384;
-// launched at 168 registers a thread: 2 x 128 x 216 + 128 x 72 = 384 x 168
-constexpr int kRegsCompute = 216, kRegsOther = 72;
 
 template <int D>
 struct Cfg {
@@ -1148,20 +1130,13 @@ __global__ void __launch_bounds__(256) window_dkv_join_kernel(const __grid_const
 
 }  // namespace dkv
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 template <int D, bool Fine>
 cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void* V, const void* O, const float* lse,
                      const void* dO, void* dQ, void* dK, void* dV, char* ws, const WinBwdPlan& p, cudaStream_t s) {
     int32_t* hdr = nullptr;
     cudaError_t e = window_error_word(&hdr);
     if (e != cudaSuccess) return e;
-    const int sms = sm_count();
+    const int sms = multiprocessors();
     const int64_t qrows = int64_t(a.B) * a.Hq * a.Lq, krows = int64_t(a.B) * a.Hk * a.Lk;
     int32_t* work = reinterpret_cast<int32_t*>(ws + p.work);
     float* nl2 = reinterpret_cast<float*>(ws + p.nl2);
@@ -1182,7 +1157,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         e = cudaFuncSetAttribute(dq::window_dq_kernel<D, Fine>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         const int nqt = (a.Lq + kTile - 1) / kTile, n = a.B * a.Hq * nqt;
-        e = launch_after(dq::window_dq_kernel<D, Fine>, n < sms ? n : sms, dq::kThreads, smem, s, tmQ, tmDO, tmK, tmV, a, n,
+        e = launch_after(dq::window_dq_kernel<D, Fine>, n < sms ? n : sms, kThreads, smem, s, tmQ, tmDO, tmK, tmV, a, n,
                          nqt, nl2, nd, work, hdr, static_cast<__nv_bfloat16*>(dQ));
         if (e != cudaSuccess) return e;
     }
@@ -1193,7 +1168,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
         const int heads = a.B * a.Hk;
         const int n = heads * (p.key_tiles - p.split_tiles + p.split_tiles * p.splits);
         if (qrows == 0) tmQ = tmDO = tmK;  // no row tile is loaded
-        e = launch_after(dkv::window_dkv_kernel<D, Fine>, n < sms ? n : sms, dkv::kThreads, smem, s, tmK, tmV, tmQ, tmDO, a,
+        e = launch_after(dkv::window_dkv_kernel<D, Fine>, n < sms ? n : sms, kThreads, smem, s, tmK, tmV, tmQ, tmDO, a,
                          p, n, nl2, nd, work + 1, hdr, parts, static_cast<__nv_bfloat16*>(dK), static_cast<__nv_bfloat16*>(dV));
         if (e != cudaSuccess) return e;
         if (p.splits > 1) {
@@ -1228,7 +1203,7 @@ WinBwdPlan plan_window_bwd(const WinArgs& a, int d) {
         const int64_t reach = (a.left == kWinOpen ? a.Lq : a.left) + (a.right == kWinOpen ? a.Lq : a.right);
         const int64_t near = (reach + kTile - 1) / kTile + 1;
         int64_t n = (all + near - 1) / near;
-        const int64_t cap = (4 * int64_t(sm_count()) + p.split_tiles * heads - 1) / (p.split_tiles * heads);
+        const int64_t cap = (4 * int64_t(multiprocessors()) + p.split_tiles * heads - 1) / (p.split_tiles * heads);
         if (n > cap) n = cap;
         p.splits = int(n < 1 ? 1 : n);
     }

@@ -331,9 +331,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     const int smem = Cfg<D>::kSmem;
     e = cudaFuncSetAttribute(window_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = multiprocessors();
     // Split the keys over a cluster until there are four CTAs an SM (two are resident;
     // the others even out streams of unlike lengths), while every CTA keeps two tiles.
     const int64_t heads = int64_t(a.B) * a.Hk;

@@ -65,10 +65,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
-// launched at 168 registers a thread (384 x 168 = 64512): softmax warpgroups 216,
-// the loading / issuing one 72: 2 x 128 x 216 + 128 x 72 = 64512
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+using win::kRegsCompute;
+using win::kRegsOther;
+using win::kThreads;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kRowsItem = 256;
 constexpr float kLazy = 8.f;  // O is rescaled once the row max grows by more than 2^8
@@ -103,15 +102,10 @@ struct Shared {  // at oBar + 176
 };
 static_assert(B_COUNT * 8 <= 176, "barriers");
 
-// An item, and one of its two row tiles. Each role keeps the tiles in scalars (an
-// index that the compiler cannot see through would put them in local memory).
-struct Item {
-    int b, hq, t0;    // first row
-    int end;          // one past the last live row (<= t0: none)
-    win::Seq seq;
-    win::Span all;    // key tiles
-    int tiles;
-};
+using win::Item;
+using win::nth_item;
+// One of an item's two row tiles. Each role keeps both in scalars (an index that the
+// compiler cannot see through would put them in local memory).
 struct QTile {
     int rows;         // live rows
     win::Span y;
@@ -119,39 +113,21 @@ struct QTile {
     __device__ __forceinline__ bool sees(int key0, int end) const { return last >= 0 && win::meets(y, key0, end); }
 };
 
-// Items of one position range lie next to each other over the heads; the last rows
-// (the longest spans under an open causal window) come first.
 __device__ __forceinline__ void decode(const WinArgs& a, int item, Item& x) {
-    const int nqt = (a.Lq + kRowsItem - 1) / kRowsItem;
-    const int heads = a.B * a.Hq;
-    const int qt = nqt - 1 - item / heads, bh = item % heads;
-    x.b = bh / a.Hq;
-    x.hq = bh - x.b * a.Hq;
-    x.t0 = qt * kRowsItem;
-    x.seq = win::seq(a, x.b);
-    x.end = min(x.t0 + kRowsItem, x.seq.m);
-    x.all = win::Span{0, 0, 0, 0, 0};
-    if (x.end > x.t0) x.all = win::span(a, x.seq, x.t0, x.end);
-    x.tiles = x.all.na + x.all.nb;
+    win::decode(a, kRowsItem, (a.Lq + kRowsItem - 1) / kRowsItem, item, x);
 }
 __device__ __forceinline__ QTile tile_of(const WinArgs& a, const Item& x, int q) {
     QTile t;
-    const int r0 = x.t0 + 128 * q, r1 = min(r0 + 128, x.end);
+    const int r0 = x.t0 + 128 * q, r1 = min(r0 + 128, x.t0 + x.rows);
     t.rows = max(r1 - r0, 0);
     t.y = win::Span{0, 0, 0, 0, 0};
     t.last = -1;
     if (t.rows > 0) {
         t.y = win::span(a, x.seq, r0, r1);
         const int key = max(t.y.a1, t.y.b1) - 1;  // its last key lies in one of the item's runs
-        if (key >= 0) t.last = x.all.nb > 0 && key >= x.all.b0 ? x.all.na + (key - x.all.b0) / win::kTile : key / win::kTile;
+        if (key >= 0) t.last = x.y.nb > 0 && key >= x.y.b0 ? x.y.na + (key - x.y.b0) / win::kTile : key / win::kTile;
     }
     return t;
-}
-// The k-th item of a CTA: rounds over the grid, every other one backwards, so that
-// no CTA gets the longer item of every round.
-__device__ __forceinline__ int nth_item(int k) {
-    const int g = int(gridDim.x), i = int(blockIdx.x);
-    return k * g + ((k & 1) ? g - 1 - i : i);
 }
 
 template <int D>
@@ -208,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool have[2] = {false, false};
                 for (int j = 0; j < x.tiles && !stop; ++j) {
                     int key0, end;
-                    win::tile(x.all, j, key0, end);
+                    win::tile(x.y, j, key0, end);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {  // a Q tile arrives with the first key tile that it sees
                         if (have[q] || !qt[q].sees(key0, end)) continue;
@@ -293,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool have[2] = {false, false};
                 for (int j = 0; j < tiles; ++j) {
                     int key0, end;
-                    win::tile(x.all, j, key0, end);
+                    win::tile(x.y, j, key0, end);
                     const uint32_t st = gt & 1;
                     if (gt > 0 && !wait_bar_warp(bar(B_V_FULL + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1, abort, hdr, 212)) { stop = true; break; }
                     bool k_ready = false;
@@ -349,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        regs_inc<kRegsSoftmax>();
+        regs_inc<kRegsCompute>();
         // -------------------------------------------------------------- softmax
         const int q = warp >> 2, row = tid & 127;
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
@@ -376,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool any = false;
             for (int j = 0; j < x.tiles; ++j, ++gt) {
                 int key0, end;
-                win::tile(x.all, j, key0, end);
+                win::tile(x.y, j, key0, end);
                 if (!qt.sees(key0, end)) continue;
                 if (!wait_bar_warp(bar(B_S_FULL + q), np & 1, abort, hdr, 221)) { stop = true; break; }
                 tc_fence_after();
@@ -555,9 +531,7 @@ cudaError_t launch_d(const WinArgs& a, int n_items, int sms, const void* Q, cons
 
 cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void* K, const void* V, void* O,
                               float* lse, cudaStream_t s) {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = multiprocessors();
     const int n_items = a.B * a.Hq * ((a.Lq + kRowsItem - 1) / kRowsItem);
     // Two row tiles an item keep the tensor core busy and share their keys (the single-shot
     // clip's 1,572 items: 661 against 788 us); up to three items for two SMs the one-tile

@@ -24,9 +24,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
-// launched at 168 registers a thread: 2 x 128 x 216 + 128 x 72 = 384 x 168
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+using win::kRegsCompute;
+using win::kRegsOther;
+using win::kThreads;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.f;  // O is rescaled once the row max grows by more than 2^8
 constexpr uint32_t kColO = 256;
@@ -65,30 +65,9 @@ struct Shared {  // at oBar + 240, after two answers of 16 bytes and the barrier
 };
 static_assert(32 + B_COUNT * 8 <= 240, "barriers");
 
-struct Item {
-    int b, hq, t0, rows;  // live rows (<= 0: none)
-    win::Seq seq;
-    win::Span y;
-    int tiles;
-};
-// The last rows (the longest spans under an open causal window) first.
-__device__ __forceinline__ void decode(const WinArgs& a, int nqt, int item, Item& x) {
-    const int heads = a.B * a.Hq;
-    const int qt = nqt - 1 - item / heads, bh = item % heads;
-    x.b = bh / a.Hq;
-    x.hq = bh - x.b * a.Hq;
-    x.t0 = qt * 128;
-    x.seq = win::seq(a, x.b);
-    x.rows = min(128, x.seq.m - x.t0);
-    x.y = win::Span{0, 0, 0, 0, 0};
-    if (x.rows > 0) x.y = win::span(a, x.seq, x.t0, x.t0 + x.rows);
-    x.tiles = x.y.na + x.y.nb;
-}
-// The n-th item of a CTA: rounds over the grid, every other one backwards.
-__device__ __forceinline__ int nth_item(int n) {
-    const int g = int(gridDim.x), i = int(blockIdx.x);
-    return n * g + ((n & 1) ? g - 1 - i : i);
-}
+using win::Item;
+using win::nth_item;
+__device__ __forceinline__ void decode(const WinArgs& a, int nqt, int item, Item& x) { win::decode(a, 128, nqt, item, x); }
 
 // Ask: the grid has a CTA for every item, and a running one asks for those that are not
 // launched yet; otherwise it has a CTA an SM, and its items are those of nth_item.
@@ -263,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        regs_inc<kRegsSoftmax>();
+        regs_inc<kRegsCompute>();
         // -------------------------------------------------------------- softmax
         const int wg = warp >> 2, row = tid & 127;
         const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
@@ -469,9 +448,7 @@ cudaError_t launch_d(const WinArgs& a, const void* Q, const void* K, const void*
     e = cudaFuncSetAttribute(window_tile_kernel<D, Ask>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int nqt = (a.Lq + 127) / 128, n_items = a.B * a.Hq * nqt;
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = multiprocessors();
     return launch_after(window_tile_kernel<D, Ask>, !Ask && n_items > sms ? sms : n_items, kThreads, smem, s, tmQ, tmK,
                         tmV, a, n_items, nqt, hdr, static_cast<__nv_bfloat16*>(O), lse);
 }

@@ -238,6 +238,14 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Multiprocessors of the current device.
+inline int multiprocessors() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
 // Asks the hardware for a CTA of this grid that has not been launched, to do its work
 // here: 16 bytes to dst and their count to the mbarrier. After an answer without one, no
 // more may be asked.

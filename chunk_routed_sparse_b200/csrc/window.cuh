@@ -98,6 +98,40 @@ __device__ __forceinline__ bool meets(const Span& y, int key0, int end) {
     return key0 < y.a1 || (key0 < y.b1 && end > y.b0);
 }
 
+// A work item of the kernels that own rows: up to `rows_item` consecutive rows of a query
+// head. Items of one range of rows lie next to each other over the heads; the last rows
+// (the longest spans under an open causal window) come first.
+struct Item {
+    int b, hq, t0;  // first row
+    int rows;       // live rows (<= 0: none)
+    Seq seq;
+    Span y;         // key tiles
+    int tiles;
+};
+__device__ __forceinline__ void decode(const WinArgs& a, int rows_item, int nqt, int item, Item& x) {
+    const int heads = a.B * a.Hq;
+    const int qt = nqt - 1 - item / heads, bh = item % heads;
+    x.b = bh / a.Hq;
+    x.hq = bh - x.b * a.Hq;
+    x.t0 = qt * rows_item;
+    x.seq = seq(a, x.b);
+    x.rows = min(rows_item, x.seq.m - x.t0);
+    x.y = Span{0, 0, 0, 0, 0};
+    if (x.rows > 0) x.y = span(a, x.seq, x.t0, x.t0 + x.rows);
+    x.tiles = x.y.na + x.y.nb;
+}
+// The k-th item of a CTA: rounds over the grid, every other one backwards, so that
+// no CTA gets the longer item of every round.
+__device__ __forceinline__ int nth_item(int k) {
+    const int g = int(gridDim.x), i = int(blockIdx.x);
+    return k * g + ((k & 1) ? g - 1 - i : i);
+}
+
+// The tcgen05 kernels' block: two warpgroups that compute and one that loads and issues.
+constexpr int kThreads = 384;
+constexpr int kRegsLaunch = 168, kRegsCompute = 216, kRegsOther = 72;  // registers a thread: at launch, then by role
+static_assert(256 * kRegsCompute + 128 * kRegsOther <= kThreads * kRegsLaunch, "registers of the launch");
+
 // Bits c of [0, 32) with lo <= c < hi.
 __device__ __forceinline__ uint32_t bits(int lo, int hi) {
     lo = max(lo, 0);
