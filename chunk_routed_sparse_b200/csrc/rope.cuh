@@ -12,8 +12,8 @@ namespace moc {
 constexpr int kMaxRopePairs = 64;  // d <= 128
 constexpr int kMaxRopeAxes = 4;
 
-// A rotation by value: at most 580 bytes, so it travels in the kernel's
-// parameters and no device memory belongs to it (any device, any stream).
+// A rotation by value: it travels in the kernel's parameters, and no device memory
+// belongs to it (any device, any stream).
 struct RopeTab {
     // angle per position in turns, as a 64-bit fraction: position x turn mod 2^64
     // is the exact fractional turn of any 32-bit position, near or far
@@ -24,6 +24,7 @@ struct RopeTab {
     int32_t axes;
     float factor;         // on the rotated part
 };
+static_assert(sizeof(RopeTab) == 592, "with three tensors' strides well below the 4 KB of a kernel's parameters");
 
 enum { ROW_COPY = 0, ROW_ROPE = 1, ROW_NORM = 2 };  // ROW_NORM: norm, then the rotation
 

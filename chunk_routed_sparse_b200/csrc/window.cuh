@@ -26,9 +26,10 @@ struct WinArgs {
     const int32_t* q_len;       // [B] or null: Lq
     const int32_t* kv_len;      // [B] or null: Lk
     float scale;
-    int32_t fill;               // rows past the lengths: 0 left as they were, 1 written as empty
-    int32_t joined;             // backward: O and lse go over more keys than this call's
+    int16_t fill;               // rows past the lengths: 0 left as they were, 1 written as empty
+    int16_t joined;             // backward: O and lse go over more keys than this call's
 };
+static_assert(sizeof(WinArgs) == 64, "eight bytes more cost every launch 0.3 us (tiny scene 14.0 -> 14.4 us a call)");
 
 #ifdef __CUDACC__
 namespace win {
