@@ -18,7 +18,8 @@
 // Rounding and masking as in the many-row kernel: P to bf16 before P V, sums of the
 // unrounded weights, keys past a run of visible ones never reach a product. (The rest of P
 // as a second operand: errors of O 1.00 instead of 1.35 times its own rounding's, for 2 to
-// 6 % of the time, 124.5 -> 127.4 us here. Not taken.)
+// 6 % of the time, 124.5 -> 127.4 us here. Not taken: a token's O then has the error that
+// the many-row kernels and the routed attention give it in a prompt, and not another.)
 #include "common.cuh"
 #include "pipeline.cuh"
 #include "tmap.cuh"

@@ -8,8 +8,8 @@
 // One persistent CTA per SM walks work items (up to 256 consecutive rows of a head, two
 // 128-row tiles A and B that share one key stream) in a fixed order: no counter in
 // memory, so calls on different streams and captured graphs share nothing.
-// (Items handed out by the hardware, clusterlaunchcontrol.try_cancel: 43 -> 45 us on the
-// odd padded batch, 658 -> 715 us on the clip below.)
+// (Items handed out by the hardware, clusterlaunchcontrol.try_cancel: 658 -> 715 us on the
+// clip below. Padded batches, whose items are unlike, take k_window_tile.cu.)
 //   warp 8 (one lane): TMA of Q tiles and of 128-key K and V tiles (2-stage rings).
 //   warp 9 (one lane): S_q = Q K^T and O_q += P V (P from TMEM), alternating A and
 //          B; an item's last PV and the next item's first S are issued back to back.
@@ -20,9 +20,10 @@
 //          shared memory into whole 128-byte row pieces.
 // Single-shot clip (12 heads, 33,272 tokens, d = 128, 512 first keys and 1,560 on either
 // side; 722 GFLOP on visible pairs): 0.66 ms in short runs (1.10 PFLOP/s), 0.77 ms
-// once the 1 kW power cap holds the clock. Between tensor core (57 % busy) and
-// exponentials (58 %) each tile's chain of product, softmax and product sets the pace;
-// a share of the exponentials on the FMA pipe measured slower.
+// once the 1 kW power cap holds the clock. Neither the tensor core nor the exponentials
+// are above half busy (45 % each with 4 heads, 53 % each causal over 6,239 keys): each
+// tile's chain of product, softmax and product sets the pace; a share of the exponentials
+// on the FMA pipe measured slower.
 // A tile that one of A, B cannot see is skipped for it; a tile that every row of a
 // warp sees whole takes no masking. Keys past a tile's end are other rows' or none:
 // their scores become -inf and their V rows are zeroed in shared memory (0 x NaN).
@@ -539,8 +540,11 @@ cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void
     // 18 items 14.9 -> 11.8 us, 81 items 18.5 -> 13.7, 162 items 27.1 -> 20.6, 216 items
     // 35.4 -> 27.9; open and causal, 33 to 34 us: 108 items -> 22.8, 216 items -> 37.4; at 408
     // items the two are level). Padded batches go there whatever their size, as it hands
-    // items out by demand (24 heads, three sequences, the last empty, up to 9,000 rows: 1.0 to
-    // 1.75 times as fast; one whose rows are all alike loses what the clip loses).
+    // items out by demand and the lengths are on the device. Its time over the two-tile
+    // kernel's for 768 to 6,240 items, d = 64 / 128: lengths down to a tenth 0.57 to 1.15 /
+    // 0.51 to 1.12, down to a half 0.77 to 1.17 / 0.75 to 1.09, one sequence empty 0.85 to 1.18 /
+    // 0.76 to 1.04, within a tenth of full 1.04 to 1.21 / 0.95 to 1.13, all full 1.10 to 1.25 / 0.92 to
+    // 1.08 (a batch known to be full is better called without q_len).
     if (a.q_len || n_items <= sms + sms / 2) return launch_window_tile(a, d, Q, K, V, O, lse, s);
     return d == 128 ? launch_d<128>(a, n_items, sms, Q, K, V, O, lse, s)
                     : launch_d<64>(a, n_items, sms, Q, K, V, O, lse, s);

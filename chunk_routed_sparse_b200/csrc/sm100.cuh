@@ -219,8 +219,8 @@ __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepc
 
 // kernel<<<grid, threads, smem, s>>>(args...), whose CTAs may start while those of the
 // kernel before it in the stream end: launch latency and set-up pass under that kernel's
-// tail (window attention of the odd padded batch and its gradient, five kernels: 140.4 ->
-// 132.7 us). What another kernel of the stream wrote is read with ordinary loads or
+// tail (window attention of the odd padded batch and its gradient, five kernels: 140.4 us
+// without it, 132.7 with, when it came in). What another kernel of the stream wrote is read with ordinary loads or
 // copies: a load through const __restrict__ may be moved ahead of the wait, and ld.global.nc
 // wants memory that nothing writes while the kernel is resident.
 template <typename... P, typename... A>

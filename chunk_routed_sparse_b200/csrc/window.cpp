@@ -57,6 +57,11 @@ extern "C" moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, in
     if (B == 0 || Hq == 0 || Lq == 0) return MOC_OK;
     if (!aligned16(Q) || !aligned16(O) || (Lk > 0 && (!aligned16(K) || !aligned16(V))) || !aligned4(lse))
         return MOC_ERR_INVALID_ARG;
+    // Up to 16 query rows to a key head one CTA cluster reads the cache once for all of them;
+    // beyond, the row-tile kernels take a query head's keys in one CTA and the group's heads
+    // read them each. Open and causal, d = 128, 1 key head of 22,563 slots: 16 query heads 45 us,
+    // 24 192 us; 3 key heads of 60,000 slots, 4 query heads to each: 4 rows 106 us, 7 498 us;
+    // 3 heads of 180,512 slots: 16 rows 302 us, 17 and 64 1,481 us.
     if (int64_t(a.group) * Lq <= moc::kWinFewRows && int64_t(B) * Hk <= 65535 && Lk > 0)
         return cuda_status(moc::launch_window_few(a, d, Q, K, V, O, lse, (cudaStream_t)stream));
     return cuda_status(moc::launch_window_fwd(a, d, Q, K, V, O, lse, (cudaStream_t)stream));
