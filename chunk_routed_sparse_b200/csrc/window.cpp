@@ -10,6 +10,13 @@ moc_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOC_OK : MOC_E
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
+struct Range {
+    uintptr_t at;
+    size_t bytes;
+    Range(const void* p, size_t n) : at(reinterpret_cast<uintptr_t>(p)), bytes(p ? n : 0) {}
+    bool meets(const Range& o) const { return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes; }
+};
+
 constexpr int64_t kMaxLen = int64_t(1) << 28;   // positions and their differences with a limit of 2^30 fit 32 bits
 // rows of one tensor: a copy's row coordinate, and an item past the last, fit 32 bits
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 65536;
@@ -57,6 +64,11 @@ extern "C" moc_status moc_window_attention(int B, int Hq, int Hk, int64_t Lq, in
     if (B == 0 || Hq == 0 || Lq == 0) return MOC_OK;
     if (!aligned16(Q) || !aligned16(O) || (Lk > 0 && (!aligned16(K) || !aligned16(V))) || !aligned4(lse))
         return MOC_ERR_INVALID_ARG;
+    const size_t qn = size_t(B) * Hq * Lq, kb = size_t(B) * Hk * Lk * d * 2;
+    const Range rq(Q, qn * d * 2), ro(O, qn * d * 2), rl(lse, qn * 4), rk(K, kb), rv(V, kb);
+    // an item reads its own Q rows before it writes them; keys and values every item reads
+    if (ro.meets(rk) || ro.meets(rv) || (Q != O && ro.meets(rq)) || rl.meets(rq) || rl.meets(rk) || rl.meets(rv) || rl.meets(ro))
+        return MOC_ERR_INVALID_ARG;
     // Up to 16 query rows to a key head one CTA cluster reads the cache once for all of them;
     // beyond, the row-tile kernels take a query head's keys in one CTA and the group's heads
     // read them each. Open and causal, d = 128, 1 key head of 22,563 slots: 16 query heads 45 us,
@@ -103,6 +115,15 @@ extern "C" moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOC_ERR_INVALID_ARG;
     const moc::WinBwdPlan p = moc::plan_window_bwd(a, d);
     if (ws_bytes < p.total) return MOC_ERR_WORKSPACE_TOO_SMALL;
+    const size_t qn = size_t(B) * Hq * Lq, qb = qn * d * 2, kb = size_t(B) * Hk * Lk * d * 2;
+    const Range out[4] = {{dQ, qb}, {dK, kb}, {dV, kb}, {ws, p.total}}, in[4] = {{Q, qb}, {dO, qb}, {K, kb}, {V, kb}};
+    for (int i = 0; i < 4; ++i) {  // (O and lse are read before anything but ws is written)
+        for (const Range& r : in)
+            if (out[i].meets(r)) return MOC_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (out[i].meets(out[j])) return MOC_ERR_INVALID_ARG;
+    }
+    if (out[3].meets({O, qb}) || out[3].meets({lse, qn * 4})) return MOC_ERR_INVALID_ARG;
     return cuda_status(moc::launch_window_bwd(a, d, Q, K, V, O, lse, dO, dQ, dK, dV, static_cast<char*>(ws), p,
                                               (cudaStream_t)stream));
 }

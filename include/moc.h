@@ -529,7 +529,8 @@ moc_status moc_qk_norm_rope_bwd(const moc_rope* rope, int dtype, int B, int Hq, 
  * or written as rows that see no key (1). Keys that no row sees are not read into
  * any result, whatever they hold. (A key that only some rows of 256 see, and that
  * holds an infinity or a NaN, can reach the others of them as 0 x infinity, and
- * so is NaN there.) softmax_scale > 0, finite. Lq, Lk < 2^28,
+ * so is NaN there.) O may be Q itself; no other overlap of an output with an input or
+ * with another output is accepted. softmax_scale > 0, finite. Lq, Lk < 2^28,
  * B Hq Lq and B Hk Lk < 2^31 - 65536, B and Hq at most 65535. Asynchronous, no
  * workspace; a device-side wait that gives up is reported by
  * moc_window_device_error. */
@@ -563,8 +564,9 @@ enum { MOC_WINDOW_FILL_REST = 1, MOC_WINDOW_JOINED = 2 };
  * rows of dQ past q_len and of dK, dV past kv_len are left as they were, or set to 0
  * with MOC_WINDOW_FILL_REST in flags. (An infinity or a NaN in a key that only some rows of 128
  * see can reach dQ of the others of them as 0 x infinity, and one in Q or dO of a
- * row that sees only some keys of 128 dK and dV of the others.) ws: 256-byte
- * aligned, contents free before and after; two calls that may overlap need two.
+ * row that sees only some keys of 128 dK and dV of the others.) dQ, dK, dV and ws
+ * overlap neither one another nor an input, but for O and lse, which dQ, dK and dV
+ * may overwrite. ws: 256-byte aligned, contents free before and after; two calls that may overlap need two.
  * Deterministic on one device model. */
 moc_status moc_window_attention_bwd(int B, int Hq, int Hk, int64_t Lq, int64_t Lk, int d, const void* Q,
                                     const void* K, const void* V, const void* O, const float* lse, const void* dO,

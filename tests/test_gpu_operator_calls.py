@@ -95,3 +95,25 @@ def test_gradient_of_the_norm_into_its_inputs_and_upstream_gradients():
         out = (q, k, u[2]) if over_inputs else tuple(u)
         got = moc.qk_norm_rope_bwd(q, k, w, w, rope, None, 1e-6, *u, out=out)
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("B,Hq,Hk,Lq,Lk,d", [(2, 4, 2, 500, 500, 64), (1, 8, 2, 3, 900, 128), (1, 30, 6, 4000, 4000, 64)])
+def test_the_output_may_be_the_queries(B, Hq, Hk, Lq, Lk, d):
+    Q, K, V = _rand(B, Hq, Lq, d, seed=1), _rand(B, Hk, Lk, d, seed=2), _rand(B, Hk, Lk, d, seed=3)
+    args = (200, 0, 40, True)
+    want = moc.window_attention_fwd(Q, K, V, *args)
+    got = moc.window_attention_fwd(Q, K, V, *args, O=Q)
+    assert got[0] is Q and torch.equal(Q, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_overlapping_outputs_are_refused():
+    Q, K, V, g = (_rand(1, 2, 200, 64, seed=i) for i in range(4))
+    with pytest.raises(moc.MocError):
+        moc.window_attention_fwd(Q, K, V, O=K)
+    O, lse = moc.window_attention_fwd(Q, K, V)
+    want = moc.window_attention_bwd(Q, K, V, O, lse, g)
+    for kw in (dict(dQ=Q), dict(dQ=g), dict(dK=K), dict(dV=g), dict(dK=O, dV=O)):
+        with pytest.raises(moc.MocError):
+            moc.window_attention_bwd(Q, K, V, O, lse, g, **kw)
+    got = moc.window_attention_bwd(Q, K, V, O, lse, g, dQ=O)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
