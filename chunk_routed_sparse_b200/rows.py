@@ -10,7 +10,10 @@ Tensors are [B, H, L, d] views in bf16, fp16 or fp32 whose last dim is dense, d 
 or 128; the other dims may have any strides (token-major projections, slots of a
 cache). ``pos`` is int32 on the same device: [L] or [axes, L] for the whole batch,
 or [B, axes, L]; None counts 0 .. L-1 for a one-axis rotation. Calls run on the
-current stream of the tensors' device.
+current stream of the tensors' device. The _fwd and _bwd calls can be captured into graphs
+freely; for a captured autograd backward torch's own rule holds, that no eager graph over
+the same leaves is alive. Gradients are reverse-mode: an input with a forward-mode tangent
+is refused.
 """
 from __future__ import annotations
 

@@ -8,8 +8,10 @@
 Q, O: contiguous bf16 [B, Hq, Lq, d]; K, V: [B, Hk, Lk, d], Hk dividing Hq, d 64 or
 128. Row t of batch entry b is at position p = t + kv_len[b] - q_len[b] and sees key
 u < kv_len[b] iff (not causal or u <= p) and (u < sinks or p - left <= u <= p + right);
-a negative left or right is no limit. q_len, kv_len: int32 [B] on the device, None for
-Lq, Lk. Calls run on the current stream of the tensors' device.
+a negative left or right is no limit (causal: right is not read). q_len, kv_len: int32 [B] on
+the device, None for Lq, Lk. Calls run on the current stream of the tensors' device. The
+_fwd and _bwd calls can be captured into graphs freely; for a captured autograd backward
+torch's own rule holds, that no eager graph over the same leaves is alive.
 """
 from __future__ import annotations
 
