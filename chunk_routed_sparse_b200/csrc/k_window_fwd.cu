@@ -543,7 +543,7 @@ cudaError_t launch_window_fwd(const WinArgs& a, int d, const void* Q, const void
     // items out by demand and the lengths are on the device. Its time over the two-tile
     // kernel's for 768 to 6,240 items, d = 64 / 128: lengths down to a tenth 0.57 to 1.15 /
     // 0.51 to 1.12, down to a half 0.77 to 1.17 / 0.75 to 1.09, one sequence empty 0.85 to 1.18 /
-    // 0.76 to 1.04, within a tenth of full 1.04 to 1.21 / 0.95 to 1.13, all full 1.10 to 1.25 / 0.92 to
+    // 0.76 to 1.04, within a tenth of full 1.04 to 1.21 / 0.98 to 1.13, all full 1.10 to 1.25 / 0.92 to
     // 1.08 (a batch known to be full is better called without q_len).
     if (a.q_len || n_items <= sms + sms / 2) return launch_window_tile(a, d, Q, K, V, O, lse, s);
     return d == 128 ? launch_d<128>(a, n_items, sms, Q, K, V, O, lse, s)
